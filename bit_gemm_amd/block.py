@@ -1,0 +1,352 @@
+"""Python binding of include/mosaicq_block.h (ctypes): the operators between a
+decoder block's 4-bit linears.
+
+    rope = Rope(128, positions=32768)                       # cos/sin table
+    cache = KVCache.empty(blocks, slots, kv_heads, 128)     # 8-bit blocks and fp16 tails
+    batch = KVBatch(cu_q, kv_len, block_table, max_new, max_len, slots=slots)
+    q = mq_kv_append(q, k, v, cache, batch, rope=rope)      # rotates q and k, writes k and v
+    o = mq_kv_attention(q, cache, batch)
+    r, h = mq_norm_residual(y, r, w_pre)                    # r' = r + y, h = norm(r') w_pre
+
+Argument marshalling only: every step runs in the HIP library, on the given
+stream (the current one by default), without synchronising. Importing this
+module fails loudly when the library is not built -- there is no fallback path.
+"""
+from __future__ import annotations
+
+import ctypes
+import os
+
+import torch
+
+from .mosaicq import MQError, STATUS, _check  # noqa: F401  (the errors of both libraries are the same)
+
+_HERE = os.path.dirname(os.path.abspath(__file__))
+LIB_PATH = os.path.join(_HERE, "libmosaicq_block.so")
+
+BLOCK = 64                                      # tokens of a cache block
+FORMATS = {torch.int8: 0, torch.float8_e4m3fn: 1}
+LAYOUTS = {"half": 0, "interleaved": 1}
+SCALINGS = {"none": 0, "linear": 1, "base": 2, "parts": 3}
+
+_vp, _i64, _i32, _f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float
+
+
+class _RopeSpec(ctypes.Structure):
+    _fields_ = [("rot_dim", _i32), ("scaling", _i32)] + [
+        (n, ctypes.c_double) for n in ("theta", "factor", "original", "turns_fast", "turns_slow")]
+
+
+class _RopePlan(ctypes.Structure):
+    _fields_ = [("table", _vp), ("positions", _i64), ("rot_dim", _i32), ("layout", _i32)]
+
+
+class _Cache(ctypes.Structure):
+    _fields_ = [(n, _vp) for n in ("k_codes", "v_codes", "k_scale", "v_scale", "k_tail", "v_tail")] + [
+        ("num_blocks", _i64), ("num_slots", _i64), ("kv_heads", _i32), ("head_dim", _i32), ("format", _i32)]
+
+
+class _Batch(ctypes.Structure):
+    _fields_ = [(n, _vp) for n in ("cu_q", "kv_len", "block_table", "slots")] + [
+        (n, _i64) for n in ("seqs", "tokens", "table_width", "max_new", "max_len")]
+
+
+class _NormArgs(ctypes.Structure):
+    _fields_ = [(n, _vp) for n in ("y", "r", "gate", "w_post", "w_pre", "r_out", "h_out")] + [
+        (n, _i64) for n in ("tokens", "width", "y_stride", "r_stride", "gate_stride", "r_out_stride", "h_stride")] + [
+        (n, _f32) for n in ("alpha", "beta", "eps", "weight_offset")] + [("residual_fp32", _i32)]
+
+
+EXPORTED = ("mq_rope_table", "mq_rope", "mq_kv_append", "mq_kv_attention", "mq_kv_attention_workspace",
+            "mq_norm_residual")
+
+
+def _load():
+    if not os.path.exists(LIB_PATH):
+        raise ImportError(f"{LIB_PATH} is not built (run `python -m bit_gemm_amd.build`)")
+    lib = ctypes.CDLL(LIB_PATH)
+    lib.mq_rope_table.argtypes = [_vp, _i64, _vp, _vp]
+    lib.mq_rope.argtypes = [_vp, _i64, _i32, _i32, _i64, _i64, _vp, _vp, _i32, _vp, _i64, _i64, _vp]
+    lib.mq_kv_append.argtypes = [_vp, _vp, _vp, _i32, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _vp]
+    lib.mq_kv_attention_workspace.argtypes = [_vp, _vp, _i32, _vp]
+    lib.mq_kv_attention.argtypes = [_vp, _vp, _vp, _i32, _i64, _i32, _f32, _vp, _i64, _vp, ctypes.c_size_t, _vp]
+    lib.mq_norm_residual.argtypes = [_vp, _vp]
+    for name in EXPORTED:
+        getattr(lib, name).restype = ctypes.c_int
+    return lib
+
+
+lib = _load()
+_F16 = torch.float16
+
+
+def _stream(stream) -> int:
+    if stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _rows(t, name: str, heads=None, dim=None):
+    """Checks an fp16 [tokens, heads, dim] GPU tensor whose rows are dense."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype is not _F16:
+        raise TypeError(f"{name} must be a float16 tensor on the GPU")
+    if t.dim() != 3 or (heads is not None and t.shape[1] != heads) or (dim is not None and t.shape[2] != dim):
+        raise ValueError(f"{name} must be [tokens, {heads or 'heads'}, {dim or 'head dim'}]")
+    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+        raise ValueError(f"the heads of a row of {name} must be dense")
+    return t
+
+
+def _row_stride(t) -> int:
+    """Elements between rows; for at most one row any stride stands, so the row's own width."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def _ints(t, name: str, shape):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype is not torch.int32 or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous int32 tensor on the GPU")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}")
+    return t
+
+
+class Rope:
+    """Cosines and sines of positions 0 .. positions - 1 for `rot_dim` rotated
+    elements (see mq_rope_table in include/mosaicq_block.h); scaling "none",
+    "linear", "base" or "parts"."""
+
+    def __init__(self, rot_dim: int, positions: int, layout: str = "half", theta: float = 10000.0,
+                 scaling: str = "none", factor: float = 1.0, original: float = 8192.0, turns_fast: float = 32.0,
+                 turns_slow: float = 1.0, stream=None):
+        if layout not in LAYOUTS or scaling not in SCALINGS:
+            raise ValueError(f"layout is one of {list(LAYOUTS)}, scaling one of {list(SCALINGS)}")
+        self.rot_dim, self.positions, self.layout = int(rot_dim), int(positions), layout
+        spec = _RopeSpec(self.rot_dim, SCALINGS[scaling], theta, factor, original, turns_fast, turns_slow)
+        self.table = torch.empty((max(self.positions, 1), max(self.rot_dim // 2, 1), 2), dtype=torch.float32,
+                                 device="cuda")
+        _check(lib.mq_rope_table(ctypes.byref(spec), self.positions, self.table.data_ptr(), _stream(stream)),
+               "mq_rope_table")
+        self._plan = _RopePlan(self.table.data_ptr(), self.positions, self.rot_dim, LAYOUTS[layout])
+        self._ref = ctypes.addressof(self._plan)
+
+
+def mq_rope(x, rope: Rope, pos, inverse: bool = False, out=None, stream=None):
+    """x [tokens, heads, head_dim] with its heads turned to positions pos
+    [tokens] int32 (turned back with inverse); out may be x. Enqueued on
+    `stream` (no sync)."""
+    if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dtype is not _F16:
+        raise TypeError("x must be a float16 tensor on the GPU")
+    if x.dim() != 3 or x.stride(2) != 1:
+        raise ValueError("x must be [tokens, heads, head_dim] with dense heads")
+    T, H, D = x.shape
+    _ints(pos, "pos", (T,))
+    if out is None:
+        out = torch.empty((T, H, D), dtype=_F16, device=x.device)
+    elif out.dtype is not _F16 or not out.is_cuda or out.shape != x.shape or out.stride(2) != 1:
+        raise ValueError("out must be a float16 GPU tensor of x's shape with dense heads")
+    _check(lib.mq_rope(x.data_ptr(), T, H, D, x.stride(0), x.stride(1), pos.data_ptr(), rope._ref, int(inverse),
+                       out.data_ptr(), out.stride(0), out.stride(1), _stream(stream)), "mq_rope")
+    return out
+
+
+class KVCache:
+    """A key/value cache in 8 bits: the tensors of mq_kv_cache (see
+    include/mosaicq_block.h). Codes are int8 or float8_e4m3fn."""
+
+    def __init__(self, k_codes, v_codes, k_scale, v_scale, k_tail, v_tail):
+        if k_codes.dtype not in FORMATS or v_codes.dtype is not k_codes.dtype:
+            raise TypeError("codes must be int8 or float8_e4m3fn tensors")
+        if k_codes.dim() != 4 or k_codes.shape[2] != BLOCK:
+            raise ValueError(f"k_codes must be [blocks, kv_heads, {BLOCK}, head_dim]")
+        nb, hk, _, D = k_codes.shape
+        if k_tail.dim() != 4:
+            raise ValueError(f"k_tail must be [slots, kv_heads, {BLOCK}, head_dim]")
+        ns = k_tail.shape[0]
+        want = {"k_codes": (k_codes, k_codes.dtype, (nb, hk, BLOCK, D)), "v_codes": (v_codes, k_codes.dtype, (nb, hk, D, BLOCK)),
+                "k_scale": (k_scale, torch.float32, (nb, hk)), "v_scale": (v_scale, torch.float32, (nb, hk)),
+                "k_tail": (k_tail, _F16, (ns, hk, BLOCK, D)), "v_tail": (v_tail, _F16, (ns, hk, D, BLOCK))}
+        for name, (t, dt, shape) in want.items():
+            if not t.is_cuda or t.dtype is not dt or not t.is_contiguous():
+                raise TypeError(f"{name} must be a contiguous {dt} tensor on the GPU")
+            if tuple(t.shape) != shape:
+                raise ValueError(f"{name} must be {list(shape)}")
+        self.k_codes, self.v_codes, self.k_scale, self.v_scale = k_codes, v_codes, k_scale, v_scale
+        self.k_tail, self.v_tail = k_tail, v_tail
+        self.num_blocks, self.num_slots, self.kv_heads, self.head_dim = nb, ns, hk, D
+        self._c = _Cache(*[t.data_ptr() for t in (k_codes, v_codes, k_scale, v_scale, k_tail, v_tail)], nb, ns, hk, D,
+                         FORMATS[k_codes.dtype])
+        self._ref = ctypes.addressof(self._c)
+
+    @classmethod
+    def empty(cls, blocks: int, slots: int, kv_heads: int, head_dim: int, fmt: str = "int8", device="cuda"):
+        """A cache of `blocks` blocks and `slots` tails, zeroed."""
+        dt = {"int8": torch.int8, "e4m3": torch.float8_e4m3fn}[fmt]
+        def z(shape, t):
+            return torch.zeros(shape, dtype=t, device=device)
+        return cls(z((blocks, kv_heads, BLOCK, head_dim), torch.int8).view(dt),
+                   z((blocks, kv_heads, head_dim, BLOCK), torch.int8).view(dt),
+                   z((blocks, kv_heads), torch.float32), z((blocks, kv_heads), torch.float32),
+                   z((slots, kv_heads, BLOCK, head_dim), _F16), z((slots, kv_heads, head_dim, BLOCK), _F16))
+
+
+class KVBatch:
+    """The sequences of one step (mq_kv_batch): cu_q [seqs + 1] where each
+    sequence's new tokens start, kv_len [seqs] its tokens with the new ones,
+    block_table [seqs, width] its cache blocks, slots [seqs] its tail slot
+    (None: the sequence's own number), all int32 on the GPU and read when the
+    kernels run. max_new and max_len bound what they hold."""
+
+    def __init__(self, cu_q, kv_len, block_table, max_new: int, max_len: int, slots=None):
+        S = kv_len.shape[0]
+        self.cu_q, self.kv_len = _ints(cu_q, "cu_q", (S + 1,)), _ints(kv_len, "kv_len", (S,))
+        if block_table.dim() != 2:
+            raise ValueError("block_table must be [seqs, width]")
+        self.block_table = _ints(block_table, "block_table", (S, block_table.shape[1]))
+        self.slots = None if slots is None else _ints(slots, "slots", (S,))
+        self.seqs, self.max_new, self.max_len = S, int(max_new), int(max_len)
+        self._c = _Batch(cu_q.data_ptr(), kv_len.data_ptr(), block_table.data_ptr(),
+                         None if slots is None else slots.data_ptr(), S, 0, block_table.shape[1], self.max_new,
+                         self.max_len)
+        self._ref = ctypes.addressof(self._c)
+        self._ws = {}      # (tokens, q heads, kv heads, head dim) -> workspace bytes
+
+    def _with(self, tokens: int) -> int:
+        self._c.tokens = tokens
+        return self._ref
+
+
+def mq_kv_append(q, k, v, cache: KVCache, batch: KVBatch, rope: Rope | None = None, q_out=None, stream=None):
+    """Writes the new tokens' k and v [tokens, kv_heads, head_dim] into the
+    cache. With a rope plan keys are turned to their positions first, and so
+    are the queries q [tokens, q_heads, head_dim] (None: no queries), which
+    are returned (in q_out where given; it may be q). Without one q is returned
+    as it is. Rows may lie apart (slices of a joined projection). Enqueued on
+    `stream` (no sync)."""
+    D, hk = cache.head_dim, cache.kv_heads
+    _rows(k, "k", hk, D)
+    _rows(v, "v", hk, D)
+    T = k.shape[0]
+    if v.shape[0] != T:
+        raise ValueError("k and v must have the same tokens")
+    qp = qo = None
+    heads = qs = qos = 0
+    if rope is not None and q is not None:
+        _rows(q, "q", None, D)
+        heads = q.shape[1]
+        if q_out is None:
+            q_out = torch.empty((T, heads, D), dtype=_F16, device=q.device)
+        else:
+            _rows(q_out, "q_out", heads, D)
+        if q.shape[0] != T or q_out.shape[0] != T:
+            raise ValueError("q, k and v must have the same tokens")
+        qp, qo, qs, qos = q.data_ptr(), q_out.data_ptr(), _row_stride(q), _row_stride(q_out)
+    if T == 0:
+        return q if qo is None else q_out
+    _check(lib.mq_kv_append(cache._ref, batch._with(T), qp, heads, qs, k.data_ptr(), _row_stride(k), v.data_ptr(),
+                            _row_stride(v), None if rope is None else rope._ref, qo, qos, _stream(stream)),
+           "mq_kv_append")
+    return q if qo is None else q_out
+
+
+def kv_attention_workspace(cache: KVCache, batch: KVBatch, tokens: int, q_heads: int) -> int:
+    """Bytes of workspace mq_kv_attention needs for these sizes."""
+    key = (tokens, q_heads, cache.kv_heads, cache.head_dim)
+    n = batch._ws.get(key)
+    if n is None:
+        out = ctypes.c_size_t()
+        _check(lib.mq_kv_attention_workspace(cache._ref, batch._with(tokens), q_heads, ctypes.byref(out)),
+               "mq_kv_attention_workspace")
+        n = batch._ws[key] = out.value
+    return n
+
+
+def mq_kv_attention(q, cache: KVCache, batch: KVBatch, causal: bool = True, scale: float | None = None, out=None,
+                    workspace=None, stream=None):
+    """softmax(scale q k^T) v of q [tokens, q_heads, head_dim] over the cache
+    (scale: head_dim^-1/2 by default), causal with the last new token at the
+    sequence's end, or over all cached tokens. workspace: a uint8 GPU tensor of
+    at least kv_attention_workspace bytes (None: taken from torch's allocator).
+    Enqueued on `stream` (no sync)."""
+    D = cache.head_dim
+    _rows(q, "q", None, D)
+    T, H = q.shape[0], q.shape[1]
+    if out is None:
+        out = torch.empty((T, H, D), dtype=_F16, device=q.device)
+    else:
+        _rows(out, "out", H, D)
+        if out.shape[0] != T:
+            raise ValueError("out must have q's tokens")
+    if T == 0:
+        return out
+    need = kv_attention_workspace(cache, batch, T, H)
+    if workspace is None:
+        ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+        if ws is not None and stream is not None:   # its memory is not given out again before the kernels are done
+            ws.record_stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
+    else:
+        if workspace.dtype is not torch.uint8 or not workspace.is_cuda or not workspace.is_contiguous():
+            raise TypeError("workspace must be a contiguous uint8 tensor on the GPU")
+        ws = workspace
+    _check(lib.mq_kv_attention(cache._ref, batch._with(T), q.data_ptr(), H, _row_stride(q), int(causal),
+                               D ** -0.5 if scale is None else scale, out.data_ptr(), _row_stride(out),
+                               None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(),
+                               _stream(stream)), "mq_kv_attention")
+    return out
+
+
+def mq_norm_residual(y, r, w_pre, w_post=None, gate=None, alpha: float = 1.0, beta: float = 1.0, eps: float = 1e-6,
+                     weight_offset: float = 0.0, r_out=None, h_out=None, stream=None):
+    """(r', h): r' = alpha r + beta gate N(y) and h = norm(r') (w_pre + offset),
+    N the norm with w_post (None: the branch as it is). y None: r' is r and
+    only h is made; w_pre None: only r' is made (h is None). y [tokens, width]
+    float16, r float16 or float32, gate [tokens, width] (expanded over tokens
+    where all share it) or [width]; r_out may be r. Enqueued on `stream` (no
+    sync)."""
+    if not isinstance(r, torch.Tensor) or not r.is_cuda or r.dtype not in (_F16, torch.float32):
+        raise TypeError("r must be a float16 or float32 tensor on the GPU")
+    if r.dim() != 2 or r.stride(1) != 1:
+        raise ValueError("r must be [tokens, width] with dense rows")
+    M, W = r.shape
+
+    def mat(t, name, dt):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype is not dt:
+            raise TypeError(f"{name} must be a {dt} tensor on the GPU")
+        if t.shape != r.shape or t.stride(1) != 1:
+            raise ValueError(f"{name} must be [{M}, {W}] with dense rows")
+        return t.data_ptr(), t.stride(0) if M > 1 else W
+
+    def vec(t, name):
+        if t is None:
+            return None
+        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype is not _F16 or not t.is_contiguous():
+            raise TypeError(f"{name} must be a contiguous float16 tensor on the GPU")
+        if t.dim() != 1 or t.shape[0] != W:
+            raise ValueError(f"{name} must be [{W}]")
+        return t.data_ptr()
+
+    yp = gp = rp = hp = None
+    ys = gs = rs = hs = 0
+    if y is not None:
+        yp, ys = mat(y, "y", _F16)
+        if r_out is None:
+            r_out = torch.empty((M, W), dtype=r.dtype, device=r.device)
+        rp, rs = mat(r_out, "r_out", r.dtype)
+        if gate is not None:
+            if gate.dim() == 1:
+                gp = vec(gate, "gate")
+            else:
+                gp, gs = mat(gate, "gate", _F16)
+    else:
+        r_out = r
+    if w_pre is not None:
+        if h_out is None:
+            h_out = torch.empty((M, W), dtype=_F16, device=r.device)
+        hp, hs = mat(h_out, "h_out", _F16)
+    else:
+        h_out = None
+    if M == 0:
+        return r_out, h_out
+    a = _NormArgs(yp, r.data_ptr(), gp, vec(w_post, "w_post") if yp else None, vec(w_pre, "w_pre"), rp, hp, M, W, ys,
+                  r.stride(0) if M > 1 else W, gs, rs, hs, alpha, beta, eps, weight_offset, r.dtype is torch.float32)
+    _check(lib.mq_norm_residual(ctypes.byref(a), _stream(stream)), "mq_norm_residual")
+    return r_out, h_out

@@ -2,7 +2,8 @@
 
     python -m bit_gemm_amd.build
 
-produces bit_gemm_amd/libmosaicq.so (the C ABI of include/mosaicq.h) and
+produces bit_gemm_amd/libmosaicq.so (the C ABI of include/mosaicq.h),
+bit_gemm_amd/libmosaicq_block.so (the C ABI of include/mosaicq_block.h) and
 bit_gemm_amd/libmq_hostcheck.so (the packer's integer arithmetic built for
 the host, used by CPU tests). Every call recompiles.
 """
@@ -19,8 +20,10 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmosaicq.so")
+BLOCK_LIB = os.path.join(HERE, "libmosaicq_block.so")
 HOSTCHECK = os.path.join(HERE, "libmq_hostcheck.so")
 SOURCES = ["api.cpp", "pack.hip", "pack_blocks.hip", "gemv.hip", "gemm.hip", "gemm_mid.hip", "gemm_rw.hip", "residual.hip", "migrate.hip", "w4a4.hip", "probe.hip"]
+BLOCK_SOURCES = ["block_api.cpp", "rope.hip", "norm.hip", "kv_append.hip", "kv_attn.hip"]
 # per-source code generation options: the prefill GEMM's stage body is one
 # long basic block; the ILP-oriented machine scheduler interleaves its
 # widening arithmetic with the MFMAs instead of clustering it after them
@@ -53,23 +56,22 @@ def _run(cmd):
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     cc = hipcc()
-    objs = []
+    obj_of = {src: os.path.join(BUILD, os.path.splitext(src)[0] + ".o") for src in SOURCES + BLOCK_SOURCES}
     cmds = []
-    for src in SOURCES:
-        obj = os.path.join(BUILD, os.path.splitext(src)[0] + ".o")
-        objs.append(obj)
+    for src, obj in obj_of.items():
         cmds.append([cc, "-x", "hip", *_flags(), *EXTRA.get(src, []), "-c", os.path.join(CSRC, src), "-o", obj])
     with ThreadPoolExecutor(max_workers=min(4, len(cmds))) as ex:
         list(ex.map(_run, cmds))
-    tmp = LIB + ".tmp"
-    _run([cc, "-shared", "-fPIC", f"--offload-arch={ARCH}", "-o", tmp, *objs])
-    os.replace(tmp, LIB)
+    for lib, sources in ((LIB, SOURCES), (BLOCK_LIB, BLOCK_SOURCES)):
+        tmp = lib + ".tmp"
+        _run([cc, "-shared", "-fPIC", f"--offload-arch={ARCH}", "-o", tmp, *[obj_of[src] for src in sources]])
+        os.replace(tmp, lib)
     tmp = HOSTCHECK + ".tmp"
     _run(["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", "-I", CSRC,
           os.path.join(CSRC, "hostcheck.cpp"), "-o", tmp])
     os.replace(tmp, HOSTCHECK)
     if verbose:
-        print(f"built {LIB} and {HOSTCHECK}")
+        print(f"built {LIB}, {BLOCK_LIB} and {HOSTCHECK}")
     return LIB
 
 

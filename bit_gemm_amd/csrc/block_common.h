@@ -1,0 +1,76 @@
+// Device helpers shared by the block operators' kernels.
+#pragma once
+#include "block_internal.h"
+#include "kernel_common.h"
+
+namespace mq {
+
+// The sequence a workgroup works on, from the device arrays, clamped to what
+// the arrays hold: a wrong length or offset cannot lead outside them.
+struct Seq {
+  int q0;     // its first new token (row of q, k, v)
+  int n;      // its new tokens
+  int len;    // its tokens, the new ones counted
+  int cap;    // those of them that the block table has room for
+  int slot;   // its tail slot, -1 where the table names none that exists
+};
+
+__device__ __forceinline__ Seq seq_of(const BatchView& b, const KvView& kv, int s) {
+  Seq q;
+  const int c0 = b.cu[s], c1 = b.cu[s + 1];
+  q.q0 = min(max(c0, 0), b.tokens);
+  q.n = min(max(c1, q.q0), b.tokens) - q.q0;
+  q.len = max(b.len[s], 0);
+  q.cap = (int)min((int64_t)q.len, (int64_t)b.width * kKvBlock);
+  const int slot = b.slot ? b.slot[s] : s;
+  q.slot = (unsigned)slot < (unsigned)kv.slots ? slot : -1;
+  return q;
+}
+
+// v, as an fp32 value of its own: a conversion to fp16 behind it cannot be
+// folded into the operation that made it, which would round once where the
+// definition rounds twice, in some instances of a kernel and not in others.
+__device__ __forceinline__ float fp32(float v) {
+  asm("" : "+v"(v));
+  return v;
+}
+
+// One pair turned: products and sums are rounded one by one (no fused
+// multiply-add), so that the result is that of the formula in fp32 whatever
+// the compiler does around it; a code of the cache then depends on the inputs
+// alone.
+__device__ __forceinline__ float2 turn(float a, float b, float2 cs) {
+#pragma clang fp contract(off)
+  const float ac = a * cs.x, bs = b * cs.y, bc = b * cs.x, as = a * cs.y;
+  return make_float2(fp32(ac - bs), fp32(bc + as));
+}
+
+// (cos, sin) of pair i at position p; NaN outside the table.
+__device__ __forceinline__ float2 cos_sin(const RopeView& r, int64_t p, int i) {
+  if ((uint64_t)p >= (uint64_t)r.positions) return make_float2(__builtin_nanf(""), __builtin_nanf(""));
+  return r.table[p * (r.rot >> 1) + i];
+}
+
+// Element d of a head row x, turned to position p.
+__device__ __forceinline__ _Float16 turned(const _Float16* x, int d, const RopeView& r, int64_t p) {
+  if (d >= r.rot) return x[d];
+  const int half = r.rot >> 1;
+  int a, b, i;
+  if (r.interleaved) {
+    i = d >> 1;
+    a = d & ~1;
+    b = a + 1;
+  } else {
+    i = d < half ? d : d - half;
+    a = i;
+    b = i + half;
+  }
+  const float2 y = turn((float)x[a], (float)x[b], cos_sin(r, p, i));
+  return (_Float16)(d == a ? y.x : y.y);
+}
+
+__device__ __forceinline__ bool finite_h(_Float16 v) {
+  return (__builtin_bit_cast(uint16_t, v) & 0x7C00u) != 0x7C00u;
+}
+
+}  // namespace mq

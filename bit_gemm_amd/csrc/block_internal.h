@@ -1,0 +1,71 @@
+// Internal declarations of the block operators (include/mosaicq_block.h):
+// what the host hands to the kernels, and the launchers.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <cstddef>
+#include <cstdint>
+
+#include "../../include/mosaicq_block.h"
+
+namespace mq {
+
+constexpr int kKvBlock = MQ_KV_BLOCK;
+
+struct RopeView {
+  const float2* table;   // [positions][rot / 2] (cos, sin); NULL: no rotation
+  int64_t positions;
+  int rot;
+  int interleaved;
+};
+
+struct KvView {
+  uint8_t *kc, *vc;
+  float *ks, *vs;
+  _Float16 *kt, *vt;
+  int64_t blocks;
+  int slots;
+  int hk;
+};
+
+struct BatchView {
+  const int32_t *cu, *len, *table, *slot;
+  int seqs, tokens, width;
+  int max_new, max_len;
+};
+
+// Rows of a [tokens, heads, head_dim] tensor, `stride` elements apart.
+struct RowsIn {
+  const _Float16* p;
+  int64_t stride;
+};
+struct RowsOut {
+  _Float16* p;
+  int64_t stride;
+};
+
+hipError_t launch_rope_table(const double* freq, int pairs, double mag, int64_t positions, float2* table,
+                             hipStream_t s);
+hipError_t launch_rope(const _Float16* x, int64_t tokens, int heads, int dim, int64_t xt, int64_t xh,
+                       const int32_t* pos, const RopeView& rope, int inverse, _Float16* y, int64_t yt, int64_t yh,
+                       hipStream_t s);
+// grid_too_large: set where the launch would need more than 2^31 - 1 workgroups (nothing is enqueued then)
+hipError_t launch_kv_append(const KvView& kv, int dim, int format, const BatchView& b, RowsIn q, int hq, RowsIn k,
+                            RowsIn v, const RopeView& rope, RowsOut qo, bool* grid_too_large, hipStream_t s);
+
+// How the attention of a batch is run: a rule on sizes alone (kv_attn.hip).
+struct AttnPlan {
+  int nt;             // blocks of 16 query rows a workgroup holds
+  int row_tiles;      // workgroups along the rows of the longest sequence
+  int chunk;          // cache blocks of one workgroup
+  int splits;         // workgroups along the cache of the longest sequence; 1: no workspace
+  int64_t groups;     // workgroups in all
+  size_t bytes;       // workspace
+};
+AttnPlan plan_attention(int hk, int hq, int dim, int64_t seqs, int64_t tokens, int64_t max_new, int64_t max_len);
+hipError_t launch_kv_attention(const KvView& kv, int dim, int format, const BatchView& b, RowsIn q, int hq, int causal,
+                               float scale, RowsOut out, void* ws, const AttnPlan& plan, hipStream_t s);
+
+hipError_t launch_norm_residual(const mq_norm_args& a, hipStream_t s);
+
+}  // namespace mq
