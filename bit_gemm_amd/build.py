@@ -23,7 +23,7 @@ LIB = os.path.join(HERE, "libmosaicq.so")
 BLOCK_LIB = os.path.join(HERE, "libmosaicq_block.so")
 HOSTCHECK = os.path.join(HERE, "libmq_hostcheck.so")
 SOURCES = ["api.cpp", "pack.hip", "pack_blocks.hip", "gemv.hip", "gemm.hip", "gemm_mid.hip", "gemm_rw.hip", "residual.hip", "migrate.hip", "w4a4.hip", "probe.hip"]
-BLOCK_SOURCES = ["block_api.cpp", "rope.hip", "norm.hip", "kv_append.hip", "kv_attn.hip"]
+BLOCK_SOURCES = ["block_api.cpp", "rope.hip", "norm.hip", "kv_append.hip", "kv_attn.hip", "kv_attn_rows.hip"]
 # per-source code generation options: the prefill GEMM's stage body is one
 # long basic block; the ILP-oriented machine scheduler interleaves its
 # widening arithmetic with the MFMAs instead of clustering it after them

@@ -55,7 +55,8 @@ hipError_t launch_kv_append(const KvView& kv, int dim, int format, const BatchVi
 
 // How the attention of a batch is run: a rule on sizes alone (kv_attn.hip).
 struct AttnPlan {
-  int nt;             // blocks of 16 query rows a workgroup holds
+  int waves;          // 0: the kernel for few rows; else the kernel for many, with workgroups of 4 or 8 waves
+  int nt;             // few rows: blocks of 16 query rows a workgroup holds
   int row_tiles;      // workgroups along the rows of the longest sequence
   int chunk;          // cache blocks of one workgroup
   int splits;         // workgroups along the cache of the longest sequence; 1: no workspace

@@ -22,33 +22,12 @@
 // not fill the GPU, the cache is split over workgroups, whose partial results
 // go to the workspace and are joined in split order by k_attn_join.
 // Bound by HBM: 2 head_dim bytes for each cached token and kv head.
-#include "block_common.h"
+#include <algorithm>
+
+#include "kv_attn_common.h"
 
 namespace mq {
 namespace {
-
-constexpr float kLog2e = 1.4426950408889634f;
-
-// 8 codes (two dwords) as fp16, exactly.
-template <int FMT>
-__device__ __forceinline__ half8_t widen8(uint32_t a, uint32_t b) {
-  u32x4_t r;
-  if (FMT == MQ_KV_E4M3) {
-    r.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, 1.0f, false));
-    r.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, 1.0f, true));
-    r.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 1.0f, false));
-    r.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 1.0f, true));
-  } else {
-    // code + 128 as the low byte of fp16 1024 + u, then - 1152
-    const half2_t bias = {(_Float16)1152.0f, (_Float16)1152.0f};
-    const uint32_t ua = a ^ 0x80808080u, ub = b ^ 0x80808080u, m = 0x64646464u;
-    r.x = __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2_t, __builtin_amdgcn_perm(m, ua, 0x04010400u)) - bias);
-    r.y = __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2_t, __builtin_amdgcn_perm(m, ua, 0x04030402u)) - bias);
-    r.z = __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2_t, __builtin_amdgcn_perm(m, ub, 0x04010400u)) - bias);
-    r.w = __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2_t, __builtin_amdgcn_perm(m, ub, 0x04030402u)) - bias);
-  }
-  return __builtin_bit_cast(half8_t, r);
-}
 
 // The largest of the four lanes that share l % 16, in all of them.
 __device__ __forceinline__ float max_groups(float v) {
@@ -59,18 +38,6 @@ __device__ __forceinline__ float sum_groups(float v) {
   v += __shfl_xor(v, 16);
   return v + __shfl_xor(v, 32);
 }
-
-struct AttnArgs {
-  KvView kv;
-  BatchView b;
-  RowsIn q;
-  RowsOut out;
-  int hq, group, causal;
-  float scale2;     // scale log2(e): scores are in units of the 2-based exponent
-  int row_tiles, chunk, splits;
-  float* ws_o;      // [tokens][q heads][splits][D] unnormalised sums
-  float2* ws_ml;    // [tokens][q heads][splits] (m, l); l = 0: nothing seen
-};
 
 // One block's keys and values in registers, as codes or (open block) as fp16.
 template <int D>
@@ -338,12 +305,17 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs A, int64_t rows) {
 template <int D, int FMT>
 hipError_t go(const AttnArgs& A, const AttnPlan& p, hipStream_t s) {
   const dim3 g((unsigned)p.groups), t(256);
-  switch (p.nt) {
-    case 1: k_attn_split<D, FMT, 1><<<g, t, 0, s>>>(A); break;
-    case 2: k_attn_split<D, FMT, 2><<<g, t, 0, s>>>(A); break;
-    default: k_attn_split<D, FMT, 4><<<g, t, 0, s>>>(A); break;
+  hipError_t e = hipSuccess;
+  if (p.waves) {
+    e = launch_attn_rows(A, D, FMT, p, s);
+  } else {
+    switch (p.nt) {
+      case 1: k_attn_split<D, FMT, 1><<<g, t, 0, s>>>(A); break;
+      case 2: k_attn_split<D, FMT, 2><<<g, t, 0, s>>>(A); break;
+      default: k_attn_split<D, FMT, 4><<<g, t, 0, s>>>(A); break;
+    }
+    e = hipGetLastError();
   }
-  hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
   const int64_t rows = (int64_t)A.b.tokens * A.hq;
   k_attn_join<D><<<dim3((unsigned)((rows + 3) / 4)), t, 0, s>>>(A, rows);
@@ -359,12 +331,19 @@ AttnPlan plan_attention(int hk, int hq, int dim, int64_t seqs, int64_t tokens, i
   if (max_new > tokens && tokens > 0) max_new = tokens;
   const int64_t rows = max_new * (hq / hk), blocks = up(max_len, kKvBlock);
   p.nt = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
-  p.row_tiles = (int)up(rows, 16 * p.nt);
-  // split the cache until the GPU has about 4 workgroups a CU, but leave a wave at least two blocks
-  const int64_t one = seqs * p.row_tiles * hk;
-  int64_t splits = one > 0 ? up(1024, one) : 1;
-  const int64_t most = up(blocks, 8);
-  if (splits > most) splits = most;
+  int64_t one, splits;
+  if (rows <= 64) {
+    // split the cache until the GPU has about 4 workgroups a CU, but leave a wave at least two blocks
+    p.row_tiles = (int)up(rows, 16 * p.nt);
+    one = seqs * p.row_tiles * hk;
+    splits = one > 0 ? std::min(up(1024, one), up(blocks, 8)) : 1;
+  } else {
+    // 8 waves where that fills the CUs, else 4; split while the CUs are not full, 16 blocks at least a part
+    p.waves = seqs * hk * up(rows, 256) >= 256 ? 8 : 4;
+    p.row_tiles = (int)up(rows, 32 * p.waves);
+    one = seqs * p.row_tiles * hk;
+    splits = one > 0 ? std::min(up(256, one), up(blocks, 16)) : 1;
+  }
   if (splits > 256) splits = 256;
   p.chunk = (int)up(blocks, splits);
   p.splits = (int)up(blocks, p.chunk);

@@ -1,0 +1,45 @@
+// What the attention kernels share: codes to fp16, their arguments.
+#pragma once
+#include "block_common.h"
+
+namespace mq {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// 8 codes (two dwords) as fp16, exactly.
+template <int FMT>
+__device__ __forceinline__ half8_t widen8(uint32_t a, uint32_t b) {
+  u32x4_t r;
+  if (FMT == MQ_KV_E4M3) {
+    r.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, 1.0f, false));
+    r.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, 1.0f, true));
+    r.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 1.0f, false));
+    r.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 1.0f, true));
+  } else {
+    // code + 128 as the low byte of fp16 1024 + u, then - 1152
+    const half2_t bias = {(_Float16)1152.0f, (_Float16)1152.0f};
+    const uint32_t ua = a ^ 0x80808080u, ub = b ^ 0x80808080u, m = 0x64646464u;
+    r.x = __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2_t, __builtin_amdgcn_perm(m, ua, 0x04010400u)) - bias);
+    r.y = __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2_t, __builtin_amdgcn_perm(m, ua, 0x04030402u)) - bias);
+    r.z = __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2_t, __builtin_amdgcn_perm(m, ub, 0x04010400u)) - bias);
+    r.w = __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2_t, __builtin_amdgcn_perm(m, ub, 0x04030402u)) - bias);
+  }
+  return __builtin_bit_cast(half8_t, r);
+}
+
+struct AttnArgs {
+  KvView kv;
+  BatchView b;
+  RowsIn q;
+  RowsOut out;
+  int hq, group, causal;
+  float scale2;     // scale log2(e): scores are in units of the 2-based exponent
+  int row_tiles, chunk, splits;
+  float* ws_o;      // [tokens][q heads][splits][D] unnormalised sums
+  float2* ws_ml;    // [tokens][q heads][splits] (m, l); l = 0: nothing seen
+};
+
+// The kernel for many query rows (kv_attn_rows.hip).
+hipError_t launch_attn_rows(const AttnArgs& A, int dim, int format, const AttnPlan& p, hipStream_t s);
+
+}  // namespace mq
