@@ -53,10 +53,11 @@ hipError_t launch_rope(const _Float16* x, int64_t tokens, int heads, int dim, in
 hipError_t launch_kv_append(const KvView& kv, int dim, int format, const BatchView& b, RowsIn q, int hq, RowsIn k,
                             RowsIn v, const RopeView& rope, RowsOut qo, bool* grid_too_large, hipStream_t s);
 
+constexpr int kAttnRows = 256;   // query rows a workgroup of the kernel for many rows holds
+
 // How the attention of a batch is run: a rule on sizes alone (kv_attn.hip).
 struct AttnPlan {
-  int waves;          // 0: the kernel for few rows; else the kernel for many, with workgroups of 4 or 8 waves
-  int nt;             // few rows: blocks of 16 query rows a workgroup holds
+  int nt;             // blocks of 16 query rows a workgroup holds; 0: the kernel for many rows, kAttnRows of them
   int row_tiles;      // workgroups along the rows of the longest sequence
   int chunk;          // cache blocks of one workgroup
   int splits;         // workgroups along the cache of the longest sequence; 1: no workspace

@@ -306,7 +306,7 @@ template <int D, int FMT>
 hipError_t go(const AttnArgs& A, const AttnPlan& p, hipStream_t s) {
   const dim3 g((unsigned)p.groups), t(256);
   hipError_t e = hipSuccess;
-  if (p.waves) {
+  if (p.nt == 0) {
     e = launch_attn_rows(A, D, FMT, p, s);
   } else {
     switch (p.nt) {
@@ -330,19 +330,20 @@ AttnPlan plan_attention(int hk, int hq, int dim, int64_t seqs, int64_t tokens, i
   AttnPlan p{};
   if (max_new > tokens && tokens > 0) max_new = tokens;
   const int64_t rows = max_new * (hq / hk), blocks = up(max_len, kKvBlock);
-  p.nt = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
   int64_t one, splits;
   if (rows <= 64) {
+    p.nt = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
     // split the cache until the GPU has about 4 workgroups a CU, but leave a wave at least two blocks
     p.row_tiles = (int)up(rows, 16 * p.nt);
     one = seqs * p.row_tiles * hk;
     splits = one > 0 ? std::min(up(1024, one), up(blocks, 8)) : 1;
   } else {
-    // 8 waves where that fills the CUs, else 4; split while the CUs are not full, 16 blocks at least a part
-    p.waves = seqs * hk * up(rows, 256) >= 256 ? 8 : 4;
-    p.row_tiles = (int)up(rows, 32 * p.waves);
+    // split the cache, 16 blocks at least a part, until there are about two workgroups a CU (as far as
+    // the host can tell: the tokens give the row tiles that there are, where sequences differ in length)
+    p.row_tiles = (int)up(rows, kAttnRows);
     one = seqs * p.row_tiles * hk;
-    splits = one > 0 ? std::min(up(256, one), up(blocks, 16)) : 1;
+    const int64_t tiles = std::min(seqs * p.row_tiles, tokens * (hq / hk) / kAttnRows + seqs);
+    splits = one > 0 ? std::min(up(512, tiles * hk), up(blocks, 16)) : 1;
   }
   if (splits > 256) splits = 256;
   p.chunk = (int)up(blocks, splits);
