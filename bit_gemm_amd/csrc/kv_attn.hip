@@ -14,20 +14,26 @@
 //   O^T += V^T P^T     values lie transposed in the cache, so a lane's 16
 //                      bytes are 16 tokens of one element: again the A operand.
 // Codes become fp16 in registers (exactly: int8 and e4m3 values are fp16
-// values); a block's scales multiply the fp32 scores and the fp32 product.
-// P is rounded to fp16 (relative 2^-11, and the sum l takes the unrounded
-// values); everything else is fp32.
+// values). A block's scales stay in fp32: with t = (k scale) s + log2(v scale)
+// the weights are p = 2^(t - m), so that O sums codes in units of 2^-m and no
+// block needs its own accumulator; the softmax's sum takes p / (v scale). p is
+// rounded to fp16 (relative 2^-11), its sum is not; all else is fp32.
 //
+// Bound by HBM: 2 head_dim bytes for each cached token and kv head. A wave's
+// loads are never conditional and keys of its next block are requested as soon
+// as this block's are multiplied, values likewise, so something is in flight
+// at all times; registers for three waves a SIMD.
 // The waves' results are joined in LDS in wave order. Where the sequences do
 // not fill the GPU, the cache is split over workgroups, whose partial results
-// go to the workspace and are joined in split order by k_attn_join.
-// Bound by HBM: 2 head_dim bytes for each cached token and kv head.
+// go to the workspace and are joined in a fixed order by k_attn_join.
 #include <algorithm>
 
 #include "kv_attn_common.h"
 
 namespace mq {
 namespace {
+
+constexpr int kWaves = 4;   // of a workgroup of k_attn_split
 
 // The largest of the four lanes that share l % 16, in all of them.
 __device__ __forceinline__ float max_groups(float v) {
@@ -39,30 +45,50 @@ __device__ __forceinline__ float sum_groups(float v) {
   return v + __shfl_xor(v, 32);
 }
 
-// One block's keys and values in registers, as codes or (open block) as fp16.
-template <int D>
-struct Codes {
-  uint4 k[4][D / 64], v[D / 16];
-};
-
 template <int D, int FMT, int NT>
-__global__ __launch_bounds__(256) void k_attn_split(AttnArgs A) {
+__global__ __launch_bounds__(64 * kWaves, NT == 4 ? 1 : 2) void k_attn_split(AttnArgs A) {
   constexpr int DT = D / 16, KS = D / 32;
-  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, c = lane & 15, g = lane >> 4;
-  // workgroup -> (sequence, row tile, kv head, split)
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, c = lane & 15, g = lane >> 4;
+  // workgroup -> (sequence, row tile, split, kv head)
   int w = (int)blockIdx.x;
-  const int split = w % A.splits;
-  w /= A.splits;
   const int h = w % A.kv.hk;
   w /= A.kv.hk;
+  const int split = w % A.splits;
+  w /= A.splits;
   const int rt = w % A.row_tiles, s = w / A.row_tiles;
+  // this wave's blocks: bw, bw + kWaves, ... Numbers and codes are requested whether the block exists and is coded or not
+  // (in its place one that does), so that nothing waits for them before they are used.
+  const int bw = split * A.chunk + wave, table_last = A.b.width - 1;
+  const uint32_t blocks = (uint32_t)A.kv.blocks;
+  const int32_t* table = A.b.table + (int64_t)s * A.b.width;
+  const auto id_of = [&](int b) { return table[min(b, table_last)]; };
+  const auto head_of = [&](int id) { return (int64_t)((uint32_t)id < blocks ? id : 0) * A.kv.hk + h; };
+  int id = id_of(bw), id_1 = id_of(bw + kWaves);
   const Seq sq = seq_of(A.b, A.kv, s);
   const int rows = sq.n * A.group, row0 = rt * 16 * NT;
   if (row0 >= rows) return;
   const int len = sq.cap;
 
+  const int ktok = 16 * (c >> 2) + (c & 3);   // + 4 k: the token of this lane's row of key tile k
+  uint4 kc[4][D / 64], vc[DT];
+  const auto load_keys = [&](int id) {
+    const uint8_t* p = A.kv.kc + head_of(id) * (kKvBlock * D) + ktok * D + 16 * g;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int j = 0; j < D / 64; ++j) kc[k][j] = *reinterpret_cast<const uint4*>(p + 4 * k * D + 64 * j);
+  };
+  const auto load_values = [&](int id) {
+    const uint8_t* p = A.kv.vc + head_of(id) * (kKvBlock * D) + c * kKvBlock + 16 * g;
+#pragma unroll
+    for (int d = 0; d < DT; ++d) vc[d] = *reinterpret_cast<const uint4*>(p + 16 * d * kKvBlock);
+  };
+  load_keys(id);
+  load_values(id);
+  float ks = A.kv.ks[head_of(id)], vs = A.kv.vs[head_of(id)];   // of this block, as loaded, a turn ahead
+
   // this lane's rows: where they end, and their queries as the B operand
-  int end[NT], last = 0, first_end = len;
+  int end[NT];
   half8_t qf[NT][KS];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
@@ -75,146 +101,135 @@ __global__ __launch_bounds__(256) void k_attn_split(AttnArgs A) {
 #pragma unroll
       for (int x = 0; x < 2; ++x)
         qf[t][2 * j + x] = *reinterpret_cast<const half8_t*>(qp + 64 * j + 16 * g + 8 * x);
-    const int e = A.causal ? max(len - sq.n + tok + 1, 0) : len;
-    end[t] = r < rows ? e : 0;
-    last = max(last, end[t]);
-    first_end = min(first_end, e);
+    end[t] = r >= rows ? 0 : A.causal ? max(len - sq.n + tok + 1, 0) : len;
   }
-#pragma unroll
-  for (int d = 1; d < 16; d <<= 1) {
-    last = max(last, __shfl_xor(last, d));
-    first_end = min(first_end, __shfl_xor(first_end, d));
-  }
-  last = __builtin_amdgcn_readfirstlane(last);
-  first_end = __builtin_amdgcn_readfirstlane(first_end);
-
-  const int nblk = (last + kKvBlock - 1) / kKvBlock;
-  const int b0 = split * A.chunk, b1 = min(nblk, b0 + A.chunk);
-  const int open_blk = len / kKvBlock;
+  // rows see more the later they are: the last one says how far, the first how far all see
+  const int last_row = min(rows, row0 + 16 * NT) - 1;
+  const int last = A.causal ? max(len - sq.n + last_row / A.group + 1, 0) : len;
+  const int all = A.causal ? max(len - sq.n + row0 / A.group + 1, 0) : len;
+  const int nblk = (last + kKvBlock - 1) / kKvBlock, open_blk = len / kKvBlock;
+  const int b1 = min(nblk, (split + 1) * A.chunk), coded = min(b1, open_blk);
 
   float4_t o[NT][DT];
   float m[NT], l[NT];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    m[t] = -INFINITY;
+    m[t] = kNoMax;
     l[t] = 0.0f;
 #pragma unroll
     for (int d = 0; d < DT; ++d) o[t][d] = (float4_t){0.0f, 0.0f, 0.0f, 0.0f};
   }
-
-  for (int b = b0 + wave; b < b1; b += 4) {
-    half8_t vf[DT][2];
-    float4_t sc[NT][4];
-    float ks, vs;
-    const int ktok = 16 * (c >> 2) + (c & 3);   // + 4 t: the token of this lane's row of key tile t
+  float4_t sc[NT][4];
+  half8_t pf[NT][2];
+  // The weights of block b from its scores: sc[t][k][i] is row 16 t + c, token 16 g + 4 k + i.
+  const auto weights = [&](int b, float ks, float vs) {
+    vs = vs == 0.0f ? kZeroScale : vs;
+    const float mul = ks * A.scale2, add = __builtin_amdgcn_logf(vs);
+    const bool masked = (b + 1) * kKvBlock > all;
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const int left = end[t] - b * kKvBlock - 16 * g;
+      float p[16], top = kNoMax;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        p[i] = fmaf(sc[t][i >> 2][i & 3], mul, add);
+        if (masked && i >= left) p[i] = -INFINITY;
+        top = fmaxf(top, p[i]);
+      }
+      top = max_groups(top);
+      if (__any(top > m[t])) {
+        const float now = fmaxf(m[t], top), shrink = __builtin_amdgcn_exp2f(m[t] - now);
+        m[t] = now;
+        l[t] *= shrink;
+#pragma unroll
+        for (int d = 0; d < DT; ++d) o[t][d] *= shrink;
+      }
+      float sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float e = __builtin_amdgcn_exp2f(p[i] - m[t]);
+        sum += e;
+        pf[t][i >> 3][i & 7] = (_Float16)e;
+      }
+      l[t] = fmaf(sum, __builtin_amdgcn_rcpf(vs), l[t]);
+    }
+  };
+  const auto no_scores = [&]() {
 #pragma unroll
     for (int t = 0; t < NT; ++t)
 #pragma unroll
       for (int k = 0; k < 4; ++k) sc[t][k] = (float4_t){0.0f, 0.0f, 0.0f, 0.0f};
-    if (b != open_blk) {
-      const int id0 = A.b.table[(int64_t)s * A.b.width + b];
-      const bool ok = (uint64_t)(int64_t)id0 < (uint64_t)A.kv.blocks;
-      const int64_t head = (int64_t)(ok ? id0 : 0) * A.kv.hk + h;
-      ks = ok ? A.kv.ks[head] : __builtin_nanf("");
-      vs = A.kv.vs[head];
-      const uint8_t* kp = A.kv.kc + head * (kKvBlock * D);
-      const uint8_t* vp = A.kv.vc + head * (kKvBlock * D);
-      Codes<D> cd;
+  };
+
+  int b = bw;
+  for (; b < coded; b += kWaves) {
+    no_scores();
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
+    for (int k = 0; k < 4; ++k)
 #pragma unroll
-        for (int j = 0; j < D / 64; ++j)
-          cd.k[k][j] = *reinterpret_cast<const uint4*>(kp + (ktok + 4 * k) * D + 64 * j + 16 * g);
+      for (int j = 0; j < D / 64; ++j) {
+        const half8_t a0 = widen8<FMT>(kc[k][j].x, kc[k][j].y), a1 = widen8<FMT>(kc[k][j].z, kc[k][j].w);
 #pragma unroll
-      for (int d = 0; d < DT; ++d)
-        cd.v[d] = *reinterpret_cast<const uint4*>(vp + (16 * d + c) * kKvBlock + 16 * g);
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-#pragma unroll
-        for (int j = 0; j < D / 64; ++j) {
-          const half8_t a0 = widen8<FMT>(cd.k[k][j].x, cd.k[k][j].y), a1 = widen8<FMT>(cd.k[k][j].z, cd.k[k][j].w);
-#pragma unroll
-          for (int t = 0; t < NT; ++t) {
-            sc[t][k] = mfma16(a0, qf[t][2 * j], sc[t][k]);
-            sc[t][k] = mfma16(a1, qf[t][2 * j + 1], sc[t][k]);
-          }
+        for (int t = 0; t < NT; ++t) {
+          sc[t][k] = mfma16(a0, qf[t][2 * j], sc[t][k]);
+          sc[t][k] = mfma16(a1, qf[t][2 * j + 1], sc[t][k]);
         }
-#pragma unroll
-      for (int d = 0; d < DT; ++d) {
-        vf[d][0] = widen8<FMT>(cd.v[d].x, cd.v[d].y);
-        vf[d][1] = widen8<FMT>(cd.v[d].z, cd.v[d].w);
       }
-    } else {
-      // the open block: fp16 in the sequence's tail, tokens from `left` on are not the sequence's
-      const int left = len - b * kKvBlock;
-      ks = sq.slot >= 0 ? 1.0f : __builtin_nanf("");
-      vs = 1.0f;
-      const int64_t head = ((int64_t)max(sq.slot, 0) * A.kv.hk + h) * (kKvBlock * D);
-      const _Float16* kp = A.kv.kt + head;
-      const _Float16* vp = A.kv.vt + head;
+    load_keys(id_1);
+    const float k1 = (uint32_t)id < blocks ? ks : __builtin_nanf(""), v1 = vs;
+    ks = A.kv.ks[head_of(id_1)];
+    vs = A.kv.vs[head_of(id_1)];
+    const int id_2 = id_of(b + 2 * kWaves);
+    weights(b, k1, v1);
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
+    for (int d = 0; d < DT; ++d) {
+      const half8_t a0 = widen8<FMT>(vc[d].x, vc[d].y), a1 = widen8<FMT>(vc[d].z, vc[d].w);
 #pragma unroll
-        for (int j = 0; j < D / 64; ++j)
+      for (int t = 0; t < NT; ++t) {
+        o[t][d] = mfma16(a0, pf[t][0], o[t][d]);
+        o[t][d] = mfma16(a1, pf[t][1], o[t][d]);
+      }
+    }
+    load_values(id_1);
+    id = id_1;
+    id_1 = id_2;
+  }
+  if (b == open_blk && b < b1) {
+    // the open block: fp16 in the sequence's tail; tokens from `left` on are not the sequence's and may be no numbers
+    const int left = len - b * kKvBlock;
+    const int64_t head = ((int64_t)max(sq.slot, 0) * A.kv.hk + h) * (kKvBlock * D);
+    const _Float16* kp = A.kv.kt + head + ktok * D + 16 * g;
+    const _Float16* vp = A.kv.vt + head + c * kKvBlock + 16 * g;
+    no_scores();
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const half8_t a = *reinterpret_cast<const half8_t*>(kp + (ktok + 4 * k) * D + 64 * j + 16 * g + 8 * x);
+    for (int k = 0; k < 4; ++k)
 #pragma unroll
-            for (int t = 0; t < NT; ++t) sc[t][k] = mfma16(a, qf[t][2 * j + x], sc[t][k]);
-          }
-#pragma unroll
-      for (int d = 0; d < DT; ++d)
+      for (int j = 0; j < D / 64; ++j)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          half8_t a = *reinterpret_cast<const half8_t*>(vp + (16 * d + c) * kKvBlock + 16 * g + 8 * x);
+          const half8_t a = *reinterpret_cast<const half8_t*>(kp + 4 * k * D + 64 * j + 8 * x);
 #pragma unroll
-          for (int i = 0; i < 8; ++i)   // whatever stands past the end may be no number: 0 x it is kept out
-            if (16 * g + 8 * x + i >= left) a[i] = (_Float16)0.0f;
-          vf[d][x] = a;
+          for (int t = 0; t < NT; ++t) sc[t][k] = mfma16(a, qf[t][2 * j + x], sc[t][k]);
         }
-    }
-    const float f = ks * A.scale2;
-    const bool masked = (b + 1) * kKvBlock > first_end;
+    weights(b, sq.slot >= 0 ? 1.0f : __builtin_nanf(""), 1.0f);
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      float top = -INFINITY;
-      float p[16];
+    for (int d = 0; d < DT; ++d)
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
+      for (int x = 0; x < 2; ++x) {
+        half8_t a = *reinterpret_cast<const half8_t*>(vp + 16 * d * kKvBlock + 8 * x);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float v = sc[t][k][i] * f;
-          if (masked && b * kKvBlock + 16 * g + 4 * k + i >= end[t]) v = -INFINITY;
-          p[4 * k + i] = v;
-          top = fmaxf(top, v);
-        }
-      top = fmaxf(m[t], max_groups(top));
-      const float ref = top == -INFINITY ? 0.0f : top;
-      const float shrink = __builtin_amdgcn_exp2f(m[t] - ref);
-      m[t] = top;
-      float sum = 0.0f;
-      half8_t pf[2];
+        for (int i = 0; i < 8; ++i)
+          if (16 * g + 8 * x + i >= left) a[i] = (_Float16)0.0f;
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float e = __builtin_amdgcn_exp2f(p[i] - ref);
-        sum += e;
-        pf[i >> 3][i & 7] = (_Float16)e;
+        for (int t = 0; t < NT; ++t) o[t][d] = mfma16(a, pf[t][x], o[t][d]);
       }
-      l[t] = l[t] * shrink + sum;
-#pragma unroll
-      for (int d = 0; d < DT; ++d) {
-        float4_t a = {0.0f, 0.0f, 0.0f, 0.0f};
-        a = mfma16(vf[d][0], pf[0], a);
-        a = mfma16(vf[d][1], pf[1], a);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[t][d][i] = o[t][d][i] * shrink + a[i] * vs;
-      }
-    }
   }
 
   // join the waves
-  __shared__ float sm[4][16 * NT], sl[4][16 * NT];
-  __shared__ float so[16 * NT][D + 4];
+  // few rows: every wave's sums side by side, added as they are written out; else one after the other into one place
+  constexpr int SIDES = NT == 1 ? kWaves : 1;
+  __shared__ float sm[kWaves][16 * NT], sl[kWaves][16 * NT];
+  __shared__ float so[SIDES][16 * NT][D + 4];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     l[t] = sum_groups(l[t]);
@@ -224,105 +239,118 @@ __global__ __launch_bounds__(256) void k_attn_split(AttnArgs A) {
     }
   }
   __syncthreads();
-  float top[NT], total[NT];
+  const auto top_of = [&](int r) {
+    float top = sm[0][r];
 #pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    const int r = 16 * t + c;
-    top[t] = fmaxf(fmaxf(sm[0][r], sm[1][r]), fmaxf(sm[2][r], sm[3][r]));
-    const float ref = top[t] == -INFINITY ? 0.0f : top[t];
-    total[t] = 0.0f;
-#pragma unroll
-    for (int x = 0; x < 4; ++x) total[t] += sl[x][r] * __builtin_amdgcn_exp2f(sm[x][r] - ref);
-    const float f = __builtin_amdgcn_exp2f(m[t] - ref);
-#pragma unroll
-    for (int d = 0; d < DT; ++d) o[t][d] *= f;
-  }
-  for (int x = 0; x < 4; ++x) {   // wave by wave: the sum's order is fixed
+    for (int x = 1; x < kWaves; ++x) top = fmaxf(top, sm[x][r]);
+    return top;
+  };
+  for (int x = SIDES == 1 ? 0 : wave; x < (SIDES == 1 ? kWaves : wave + 1); ++x) {   // wave by wave: the sum's order is fixed
     if (wave == x) {
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
+      for (int t = 0; t < NT; ++t) {
+        const float f = __builtin_amdgcn_exp2f(m[t] - top_of(16 * t + c));
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
-          float4_t* p = reinterpret_cast<float4_t*>(&so[16 * t + c][16 * d + 4 * g]);
-          *p = x == 0 ? o[t][d] : *p + o[t][d];
+          float4_t* p = reinterpret_cast<float4_t*>(&so[SIDES == 1 ? 0 : wave][16 * t + c][16 * d + 4 * g]);
+          *p = SIDES > 1 || x == 0 ? o[t][d] * f : *p + o[t][d] * f;
         }
+      }
     }
-    __syncthreads();
+    if (SIDES == 1) __syncthreads();
   }
-  if (wave == 0 && g == 0) {
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      sm[0][16 * t + c] = top[t];
-      sl[0][16 * t + c] = total[t];
-    }
-  }
-  __syncthreads();
-  for (int e = tid; e < 16 * NT * (D / 4); e += 256) {
+  if (SIDES > 1) __syncthreads();
+  for (int e = tid; e < 16 * NT * (D / 4); e += 64 * kWaves) {
     const int r = e / (D / 4), d = (e % (D / 4)) * 4;
     if (row0 + r >= rows) break;
     const int tok = (row0 + r) / A.group, hh = (row0 + r) % A.group;
     const int64_t row = (int64_t)(sq.q0 + tok) * A.hq + h * A.group + hh;
-    const float4_t v = *reinterpret_cast<const float4_t*>(&so[r][d]);
+    float4_t v = *reinterpret_cast<const float4_t*>(&so[0][r][d]);
+#pragma unroll
+    for (int x = 1; x < SIDES; ++x) v += *reinterpret_cast<const float4_t*>(&so[x][r][d]);
+    const float top = top_of(r);
+    float total = 0.0f;
+#pragma unroll
+    for (int x = 0; x < kWaves; ++x) total += sl[x][r] * __builtin_amdgcn_exp2f(sm[x][r] - top);
     if (A.splits == 1) {
-      const float inv = sl[0][r] == 0.0f ? 0.0f : 1.0f / sl[0][r];
+      const float inv = total == 0.0f ? 0.0f : 1.0f / total;
       store4(reinterpret_cast<uint16_t*>(A.out.p + (int64_t)(sq.q0 + tok) * A.out.stride + (int64_t)(h * A.group + hh) * D + d),
              v * inv, 4, true);
     } else {
       *reinterpret_cast<float4_t*>(A.ws_o + (row * A.splits + split) * D + d) = v;
-      if (d == 0) A.ws_ml[row * A.splits + split] = make_float2(sm[0][r], sl[0][r]);
+      if (d == 0) A.ws_ml[row * A.splits + split] = make_float2(top, total);
     }
   }
 }
 
-// Joins the splits of one (token, query head) row in split order: one wave a row.
-template <int D>
+// Joins the splits of (token, query head) rows: Y groups of threads a row, group y takes splits y, y + Y, ...; in a
+// group thread x takes elements 4 x .. 4 x + 3. The groups' sums are added in order. One group a row where the splits
+// are few and the rows many, else all of the workgroup's.
+template <int D, int Y>
 __global__ __launch_bounds__(256) void k_attn_join(AttnArgs A, int64_t rows) {
-  const int lane = threadIdx.x & 63;
-  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (row >= rows) return;
-  const float2* ml = A.ws_ml + row * A.splits;
-  float top = -INFINITY;
-  for (int x = lane; x < A.splits; x += 64) top = fmaxf(top, ml[x].x);
+  constexpr int X = D / 4, R = 256 / (X * Y);   // rows of a workgroup
+  __shared__ float4_t part[256 / X][X];
+  __shared__ float part_l[256 / X];
+  const int x = threadIdx.x % X, z = threadIdx.x / X, y = z % Y, n = A.splits;
+  const int64_t row = min((int64_t)blockIdx.x * R + z / Y, rows - 1);
+  const float2* ml = A.ws_ml + row * n;
+  const float4_t* src = reinterpret_cast<const float4_t*>(A.ws_o) + row * n * X + x;
+  float top = kNoMax;
+  for (int i = x; i < n; i += X) top = fmaxf(top, ml[i].x);
 #pragma unroll
-  for (int d = 32; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
-  const float ref = top == -INFINITY ? 0.0f : top;
-  float acc[D / 64], total = 0.0f;
-#pragma unroll
-  for (int i = 0; i < D / 64; ++i) acc[i] = 0.0f;
-  for (int x = 0; x < A.splits; ++x) {
-    const float2 v = ml[x];
-    const float f = __builtin_amdgcn_exp2f(v.x - ref);
+  for (int d = X / 2; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor(top, d));
+  float4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
+  float total = 0.0f;
+#pragma unroll 4
+  for (int i = y; i < n; i += Y) {
+    const float2 v = ml[i];
+    const float f = __builtin_amdgcn_exp2f(v.x - top);
     total += v.y * f;
+    acc += src[(int64_t)i * X] * f;
+  }
+  if (Y > 1) {
+    part[z][x] = acc;
+    if (x == 0) part_l[z] = total;
+    __syncthreads();
+    if (y != 0) return;
+    total = 0.0f;
+    acc = (float4_t){0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int i = 0; i < D / 64; ++i) acc[i] += A.ws_o[(row * A.splits + x) * D + lane + 64 * i] * f;
+    for (int i = 0; i < Y; ++i) {
+      total += part_l[z + i];
+      acc += part[z + i][x];
+    }
   }
   const float inv = total == 0.0f ? 0.0f : 1.0f / total;
   const int64_t tok = row / A.hq, hh = row % A.hq;
-#pragma unroll
-  for (int i = 0; i < D / 64; ++i) A.out.p[tok * A.out.stride + hh * D + lane + 64 * i] = (_Float16)(acc[i] * inv);
+  store4(reinterpret_cast<uint16_t*>(A.out.p + tok * A.out.stride + hh * D + 4 * x), acc * inv, 4, true);
 }
+
+int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 template <int D, int FMT>
 hipError_t go(const AttnArgs& A, const AttnPlan& p, hipStream_t s) {
-  const dim3 g((unsigned)p.groups), t(256);
+  const dim3 g((unsigned)p.groups), ts(64 * kWaves), t(256);
   hipError_t e = hipSuccess;
   if (p.nt == 0) {
     e = launch_attn_rows(A, D, FMT, p, s);
   } else {
     switch (p.nt) {
-      case 1: k_attn_split<D, FMT, 1><<<g, t, 0, s>>>(A); break;
-      case 2: k_attn_split<D, FMT, 2><<<g, t, 0, s>>>(A); break;
-      default: k_attn_split<D, FMT, 4><<<g, t, 0, s>>>(A); break;
+      case 1: k_attn_split<D, FMT, 1><<<g, ts, 0, s>>>(A); break;
+      case 2: k_attn_split<D, FMT, 2><<<g, ts, 0, s>>>(A); break;
+      default: k_attn_split<D, FMT, 4><<<g, ts, 0, s>>>(A); break;
     }
     e = hipGetLastError();
   }
   if (e != hipSuccess || p.splits == 1) return e;
   const int64_t rows = (int64_t)A.b.tokens * A.hq;
-  k_attn_join<D><<<dim3((unsigned)((rows + 3) / 4)), t, 0, s>>>(A, rows);
+  constexpr int Y = 256 / (D / 4);   // 8 or 16 groups
+  if (p.splits <= 4)
+    k_attn_join<D, 1><<<dim3((unsigned)up(rows, Y)), t, 0, s>>>(A, rows);
+  else
+    k_attn_join<D, Y><<<dim3((unsigned)rows), t, 0, s>>>(A, rows);
   return hipGetLastError();
 }
-
-int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 }  // namespace
 
@@ -336,7 +364,7 @@ AttnPlan plan_attention(int hk, int hq, int dim, int64_t seqs, int64_t tokens, i
     // split the cache until the GPU has about 4 workgroups a CU, but leave a wave at least two blocks
     p.row_tiles = (int)up(rows, 16 * p.nt);
     one = seqs * p.row_tiles * hk;
-    splits = one > 0 ? std::min(up(1024, one), up(blocks, 8)) : 1;
+    splits = one > 0 ? std::min(up(256, one), up(blocks, 2 * kWaves)) : 1;
   } else {
     // split the cache, 16 blocks at least a part, until there are about two workgroups a CU (as far as
     // the host can tell: the tokens give the row tiles that there are, where sequences differ in length)

@@ -5,6 +5,8 @@
 namespace mq {
 
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kNoMax = -1.0e30f;   // the reference before the first visible token: finite, below every score
+constexpr float kZeroScale = 1.0f / (1 << 30);   // stands for the scale of values that are all zero
 
 // 8 codes (two dwords) as fp16, exactly.
 template <int FMT>

@@ -16,8 +16,7 @@
 // needs its own accumulator; the softmax's sum takes p / (v scale). The
 // reference m follows the running maximum only when that has grown by more
 // than 2^8 (p then reaches 2^8 at most, far inside fp16), so the sums are
-// rarely rescaled. p is rounded to fp16 (relative 2^-11) and its sum, in fp32, takes the rounded
-// values, so that the weights add up to one.
+// rarely rescaled. p is rounded to fp16 (relative 2^-11), its sum is not.
 // LDS rows are swizzled by 16-byte pieces, so that lanes that read together hit
 // different banks.
 // Bound by the matrix cores and the exponentials beside them.
@@ -48,9 +47,7 @@ __device__ __forceinline__ float sum_halves(float v) {
 }
 
 constexpr int kWaves = kAttnRows / 32;
-constexpr float kNoMax = -1.0e30f;   // the reference before the first visible token: finite, below every score
 constexpr float kSlack = 8.0f;       // how far (powers of two) the maximum may run ahead of the reference
-constexpr float kZeroScale = 1.0f / (1 << 30);   // stands for the scale of values that are all zero
 
 // The swizzle of a key row and of a value row: 16-byte piece -> place. Keys of
 // 128 elements fill a line of the 64 banks, the others half of one: any 16
