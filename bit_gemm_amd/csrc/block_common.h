@@ -69,6 +69,49 @@ __device__ __forceinline__ _Float16 turned(const _Float16* x, int d, const RopeV
   return (_Float16)(d == a ? y.x : y.y);
 }
 
+// Eight pairs (half layout: a the first elements, b the second ones) or four (interleaved: a) turned by the cosines and
+// sines of NP pairs.
+template <bool INTER, int NP>
+__device__ __forceinline__ void turn_piece(half8_t& a, half8_t& b, const float2* cs) {
+#pragma unroll
+  for (int i = 0; i < NP; ++i) {
+    const float2 r = INTER ? turn((float)a[2 * i], (float)a[2 * i + 1], cs[i]) : turn((float)a[i], (float)b[i], cs[i]);
+    if (INTER) {
+      a[2 * i] = (_Float16)r.x;
+      a[2 * i + 1] = (_Float16)r.y;
+    } else {
+      a[i] = (_Float16)r.x;
+      b[i] = (_Float16)r.y;
+    }
+  }
+}
+
+// (cos, sin) of NP pairs from pair i0 on at position p, the sines times dir; NaN outside the table. NP and i0 are even,
+// so the table is read in 16-byte pieces.
+template <int NP>
+__device__ __forceinline__ void load_cos_sin(const RopeView& r, int64_t p, int i0, float dir, float2* cs) {
+  if ((uint64_t)p < (uint64_t)r.positions) {
+    const float4* row = reinterpret_cast<const float4*>(r.table + p * (r.rot >> 1) + i0);
+#pragma unroll
+    for (int i = 0; i < NP / 2; ++i) {
+      const float4 f = row[i];
+      cs[2 * i] = make_float2(f.x, f.y * dir);
+      cs[2 * i + 1] = make_float2(f.z, f.w * dir);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NP; ++i) cs[i] = make_float2(__builtin_nanf(""), __builtin_nanf(""));
+  }
+}
+
+// Whether a rotation's pairs fall into 16-byte pieces, and a tensor's rows too.
+inline bool piecewise(const RopeView& r) {
+  return r.rot % (r.interleaved ? 8 : 16) == 0 && (reinterpret_cast<uintptr_t>(r.table) & 15u) == 0;
+}
+inline bool wide_rows(const void* p, int64_t stride) {
+  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && stride % 8 == 0;
+}
+
 __device__ __forceinline__ bool finite_h(_Float16 v) {
   return (__builtin_bit_cast(uint16_t, v) & 0x7C00u) != 0x7C00u;
 }

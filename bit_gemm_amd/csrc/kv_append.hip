@@ -9,11 +9,13 @@
 //                magnitude of each gives its scale; codes are written, the
 //                values' transposed, so that the attention reads both as the
 //                matrix cores want them without a transposition of its own;
-//   open block   the workgroup of a sequence's first touched block also writes
-//                the tokens of the block that stays open into the tail: after
-//                its own reads of the tail, which may share the tail's places.
+//   open block   the tokens of the block that stays open go into the tail; by
+//                the workgroup of the first touched block where that reads the
+//                tail, after its reads, since they may take the same places.
 // Bound by HBM for prompts (rows read once, codes written once), by the chain
 // of dependent loads (offsets, position, rotation, store) for single tokens.
+#include <type_traits>
+
 #include "block_common.h"
 
 namespace mq {
@@ -30,46 +32,250 @@ __device__ __forceinline__ uint32_t code4(float a, float b, float c, float d) {
   return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(cut(c), cut(d), (int)w, true);
 }
 
+// A block's keys and values in LDS: keys as rows (padded by 16 bytes); values transposed, the tokens of an element as
+// pairs, swizzled by groups of four pairs so that neither writes along the elements nor reads along the tokens pile up
+// on a bank.
 template <int D>
 struct Tile {
-  _Float16 x[kKvBlock][D + 8];   // rows padded by 16 bytes: column reads spread over the banks
+  _Float16 k[kKvBlock][D + 8];
+  uint32_t v[D][kKvBlock / 2];
+  uint32_t top[4][2];   // largest magnitudes of the waves' keys and values
+  uint8_t bad_tok[kKvBlock];
 };
+__device__ __forceinline__ int pair_place(int d, int pair) { return pair ^ (((d >> 3) & 7) << 2); }
 
-// The 64 keys or values of block `blk` of sequence q into LDS, turned.
-template <int D, bool IS_K>
-__device__ __forceinline__ void stage(Tile<D>& t, const KvView& kv, const Seq& q, int h, int p0, RowsIn rows,
+template <int D>
+__device__ __forceinline__ void put_value(Tile<D>& t, int tok, int d, _Float16 x) {
+  reinterpret_cast<_Float16*>(&t.v[d][pair_place(d, tok >> 1)])[tok & 1] = x;
+}
+
+// The 64 keys and values of the block at p0 of sequence q into LDS, the new keys turned. VEC: new rows are read in
+// 16-byte pieces, a rotation works on whole pieces.
+template <int D, bool VEC>
+__device__ __forceinline__ void stage(Tile<D>& t, const KvView& kv, const Seq& q, int h, int p0, RowsIn kr, RowsIn vr,
                                       const RopeView& rope) {
-  const int before = q.len - q.n;   // tokens that were there
+  const int tid = threadIdx.x, before = q.len - q.n;   // tokens that were there
   const int have = min(max(before - p0, 0), kKvBlock);
-  if (have > 0) {
-    const int64_t base = ((int64_t)max(q.slot, 0) * kv.hk + h) * kKvBlock * D;
-    for (int e = threadIdx.x; e < kKvBlock * D; e += 256) {
-      const int tok = IS_K ? e / D : e % kKvBlock, d = IS_K ? e % D : e / kKvBlock;
-      if (tok < have) t.x[tok][d] = (IS_K ? kv.kt : kv.vt)[base + e];
+  const _Float16* kx = kr.p + (int64_t)(q.q0 + p0 - before) * kr.stride + (int64_t)h * D;   // token 0's row, new or not
+  const _Float16* vx = vr.p + (int64_t)(q.q0 + p0 - before) * vr.stride + (int64_t)h * D;
+  if (VEC) {
+    // values: the same piece of two tokens, so that a pair is written whole (half of it may be an older token's, below)
+    constexpr int VP = kKvBlock / 2 * (D / 8) / 256;
+    half8_t va[VP], vb[VP];
+#pragma unroll
+    for (int i = 0; i < VP; ++i) {
+      const int e = tid + 256 * i, pair = e / (D / 8), d = 8 * (e % (D / 8));
+      va[i] = vb[i] = (half8_t)(_Float16)0.0f;
+      if (2 * pair >= have) va[i] = *reinterpret_cast<const half8_t*>(vx + (int64_t)(2 * pair) * vr.stride + d);
+      if (2 * pair + 1 >= have) vb[i] = *reinterpret_cast<const half8_t*>(vx + (int64_t)(2 * pair + 1) * vr.stride + d);
+    }
+    const int half = rope.rot >> 1, turns = !rope.table ? 0 : rope.interleaved ? rope.rot >> 3 : rope.rot >> 4;
+    const int rest = rope.table ? (D - rope.rot) >> 3 : D / 8, units = turns + rest;
+    const auto key_piece = [&](int tok, int d) {
+      return *reinterpret_cast<const half8_t*>(kx + (int64_t)tok * kr.stride + d);
+    };
+    for (int e = tid; e < kKvBlock * units; e += 256) {
+      const int tok = e / units, u = e % units;
+      if (tok < have) continue;
+      if (u >= turns) {
+        const int d = (rope.table ? rope.rot : 0) + 8 * (u - turns);
+        *reinterpret_cast<half8_t*>(&t.k[tok][d]) = key_piece(tok, d);
+      } else if (rope.interleaved) {
+        half8_t a = key_piece(tok, 8 * u);
+        float2 cs[4];
+        load_cos_sin<4>(rope, p0 + tok, 4 * u, 1.0f, cs);
+        turn_piece<true, 4>(a, a, cs);
+        *reinterpret_cast<half8_t*>(&t.k[tok][8 * u]) = a;
+      } else {
+        half8_t a = key_piece(tok, 8 * u), b = key_piece(tok, 8 * u + half);
+        float2 cs[8];
+        load_cos_sin<8>(rope, p0 + tok, 8 * u, 1.0f, cs);
+        turn_piece<false, 8>(a, b, cs);
+        *reinterpret_cast<half8_t*>(&t.k[tok][8 * u]) = a;
+        *reinterpret_cast<half8_t*>(&t.k[tok][8 * u + half]) = b;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < VP; ++i) {
+      const int e = tid + 256 * i, pair = e / (D / 8), d = 8 * (e % (D / 8));
+#pragma unroll
+      for (int x = 0; x < 8; ++x)
+        t.v[d + x][pair_place(d, pair)] = (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)va[i][x]) |
+                                          (uint32_t)__builtin_bit_cast(uint16_t, (_Float16)vb[i][x]) << 16;
+    }
+    if (have > 0) __syncthreads();   // the older tokens' halves of pairs come after
+  } else {
+    for (int e = tid; e < kKvBlock * D; e += 256) {
+      const int tok = e / D, d = e % D;
+      if (tok < have) continue;
+      const _Float16* x = kx + (int64_t)tok * kr.stride;
+      t.k[tok][d] = rope.table ? turned(x, d, rope, p0 + tok) : x[d];
+      put_value(t, tok, d, vx[(int64_t)tok * vr.stride + d]);
     }
   }
-  for (int e = threadIdx.x; e < kKvBlock * D; e += 256) {
-    const int tok = e / D, d = e % D;
-    if (tok >= have) {
-      const _Float16* x = rows.p + (int64_t)(q.q0 + p0 + tok - before) * rows.stride + (int64_t)h * D;
-      t.x[tok][d] = IS_K && rope.table ? turned(x, d, rope, p0 + tok) : x[d];
+  if (have > 0) {   // the block's earlier tokens, turned when they came
+    const int64_t base = ((int64_t)max(q.slot, 0) * kv.hk + h) * kKvBlock * D;
+    for (int e = tid; e < have * (D / 8); e += 256) {
+      const int tok = e / (D / 8), d = 8 * (e % (D / 8));
+      *reinterpret_cast<half8_t*>(&t.k[tok][d]) = *reinterpret_cast<const half8_t*>(kv.kt + base + (int64_t)tok * D + d);
+    }
+    for (int e = tid; e < D * 8; e += 256) {
+      const int d = e >> 3, tok = 8 * (e & 7);
+      if (tok >= have) continue;
+      const half8_t x = *reinterpret_cast<const half8_t*>(kv.vt + base + (int64_t)d * kKvBlock + tok);
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (tok + i < have) put_value(t, tok + i, d, x[i]);
     }
   }
 }
 
+// Largest magnitude of 16 fp16 values, as its bits: the order of the bits is that of the magnitudes, and what is not
+// finite lies above all that is.
+__device__ __forceinline__ uint32_t top_bits(const half8_t& a, const half8_t& b, uint32_t top) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t x = __builtin_bit_cast(uint16_t, (_Float16)a[i]) & 0x7FFFu;
+    const uint32_t y = __builtin_bit_cast(uint16_t, (_Float16)b[i]) & 0x7FFFu;
+    top = max(top, max(x, y));
+  }
+  return top;
+}
+
+template <int FMT>
+__device__ __forceinline__ uint4 code16(const half8_t& a, const half8_t& b, float inv) {
+  uint4 w;
+  w.x = code4<FMT>((float)a[0] * inv, (float)a[1] * inv, (float)a[2] * inv, (float)a[3] * inv);
+  w.y = code4<FMT>((float)a[4] * inv, (float)a[5] * inv, (float)a[6] * inv, (float)a[7] * inv);
+  w.z = code4<FMT>((float)b[0] * inv, (float)b[1] * inv, (float)b[2] * inv, (float)b[3] * inv);
+  w.w = code4<FMT>((float)b[4] * inv, (float)b[5] * inv, (float)b[6] * inv, (float)b[7] * inv);
+  return w;
+}
+
+// Scales and codes of the block in LDS into block `id` of head h: a thread codes pieces of 16 elements of the keys' rows
+// and of the values' columns, contiguous in memory over the lanes.
 template <int D, int FMT>
-__global__ __launch_bounds__(256) void k_append(KvView kv, BatchView b, RowsIn qr, int hq, RowsIn kr, RowsIn vr,
-                                                RopeView rope, RowsOut qo, int touched, int kv_groups,
-                                                int q_tokens, int q_groups) {
+__device__ __forceinline__ void code_block(Tile<D>& t, const KvView& kv, int64_t id, int h) {
   constexpr float kMax = FMT == MQ_KV_INT8 ? 127.0f : 448.0f;
+  constexpr int P = kKvBlock * D / 16 / 256;   // pieces of a thread
   const int tid = threadIdx.x;
-  if ((int)blockIdx.x >= kv_groups) {   // queries
-    const int w = (int)blockIdx.x - kv_groups;
-    const int s = w / q_groups, t0 = (w % q_groups) * q_tokens;
-    const Seq q = seq_of(b, kv, s);
-    const int t1 = min(q.n, t0 + q_tokens);
+  half8_t k[P][2], v[P][2];
+  uint32_t kt = 0, vt = 0;
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    const int p = tid + 256 * i, tok = p / (D / 16), kd = 16 * (p % (D / 16)), d = p / 4, pair = 8 * (p % 4);
+    k[i][0] = *reinterpret_cast<const half8_t*>(&t.k[tok][kd]);
+    k[i][1] = *reinterpret_cast<const half8_t*>(&t.k[tok][kd + 8]);
+    v[i][0] = *reinterpret_cast<const half8_t*>(&t.v[d][pair_place(d, pair)]);
+    v[i][1] = *reinterpret_cast<const half8_t*>(&t.v[d][pair_place(d, pair + 4)]);
+    kt = top_bits(k[i][0], k[i][1], kt);
+    vt = top_bits(v[i][0], v[i][1], vt);
+  }
+  const auto join = [&]() {
+#pragma unroll
+    for (int d = 32; d > 0; d >>= 1) {
+      kt = max(kt, (uint32_t)__shfl_xor((int)kt, d));
+      vt = max(vt, (uint32_t)__shfl_xor((int)vt, d));
+    }
+    if ((tid & 63) == 0) {
+      t.top[tid >> 6][0] = kt;
+      t.top[tid >> 6][1] = vt;
+    }
+    __syncthreads();
+    kt = max(max(t.top[0][0], t.top[1][0]), max(t.top[2][0], t.top[3][0]));
+    vt = max(max(t.top[0][1], t.top[1][1]), max(t.top[2][1], t.top[3][1]));
+  };
+  join();
+  const bool bad = kt >= 0x7C00u || vt >= 0x7C00u;
+  if (bad) {
+    // rare: vectors that are not finite. Their key rows count as zeros, and so do the values that are no numbers.
+    if (tid < kKvBlock) t.bad_tok[tid] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      const int p = tid + 256 * i, tok = p / (D / 16), vtok = 16 * (p % 4);
+      if (top_bits(k[i][0], k[i][1], 0) >= 0x7C00u) t.bad_tok[tok] = 1;
+#pragma unroll
+      for (int x = 0; x < 16; ++x) {
+        if (!finite_h(v[i][x >> 3][x & 7])) {
+          t.bad_tok[vtok + x] = 1;
+          v[i][x >> 3][x & 7] = (_Float16)0.0f;
+        }
+      }
+    }
+    __syncthreads();
+    kt = vt = 0;
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      if (t.bad_tok[(tid + 256 * i) / (D / 16)]) k[i][0] = k[i][1] = (half8_t)(_Float16)0.0f;
+      kt = top_bits(k[i][0], k[i][1], kt);
+      vt = top_bits(v[i][0], v[i][1], vt);
+    }
+    join();
+  }
+  const float km = h_to_f(kt), vm = h_to_f(vt);
+  const float ki = km > 0.0f ? kMax * (1.0f / km) : 0.0f, vi = vm > 0.0f ? kMax * (1.0f / vm) : 0.0f;
+  const int64_t head = id * kv.hk + h;
+  uint4* ko = reinterpret_cast<uint4*>(kv.kc + head * (kKvBlock * D));
+  uint4* vo = reinterpret_cast<uint4*>(kv.vc + head * (kKvBlock * D));
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    ko[tid + 256 * i] = code16<FMT>(k[i][0], k[i][1], ki);
+    vo[tid + 256 * i] = code16<FMT>(v[i][0], v[i][1], vi);
+  }
+  if (tid == 0) {
+    // the keys carry the mark of a vector that is not finite: a NaN scale makes the head's scores NaN for the rows that
+    // attend to the block, and masked scores are replaced before use
+    kv.ks[head] = bad ? __builtin_nanf("") : km / kMax;
+    kv.vs[head] = vm / kMax;
+  }
+}
+
+// Queries of one sequence: tokens t0 .. t1 - 1 turned.
+template <int D, bool VEC>
+__device__ __forceinline__ void turn_queries(const Seq& q, int t0, int t1, int hq, RowsIn qr, RowsOut qo,
+                                             const RopeView& rope) {
+  const int64_t pos0 = (int64_t)q.len - q.n;
+  if (VEC) {
+    constexpr int HP = 4;   // heads that share the cosines and sines a thread loads
+    const int half = rope.rot >> 1, turns = rope.interleaved ? rope.rot >> 3 : rope.rot >> 4;
+    const int units = turns + ((D - rope.rot) >> 3), hg = (hq + HP - 1) / HP, per = hg * units;
+    for (int e = threadIdx.x; e < (t1 - t0) * per; e += 256) {
+      const int tok = t0 + e / per, rest = e % per, h0 = rest / units * HP, u = rest % units;
+      const _Float16* x = qr.p + (int64_t)(q.q0 + tok) * qr.stride + (int64_t)h0 * D;
+      _Float16* y = qo.p + (int64_t)(q.q0 + tok) * qo.stride + (int64_t)h0 * D;
+      const bool pass = u >= turns;
+      const int d = pass ? rope.rot + 8 * (u - turns) : 8 * u;
+      const bool two = !pass && !rope.interleaved;
+      half8_t a[HP], b[HP];
+#pragma unroll
+      for (int h = 0; h < HP; ++h) {
+        if (h0 + h < hq) {
+          a[h] = *reinterpret_cast<const half8_t*>(x + h * D + d);
+          if (two) b[h] = *reinterpret_cast<const half8_t*>(x + h * D + d + half);
+        }
+      }
+      float2 cs[8];
+      if (two)
+        load_cos_sin<8>(rope, pos0 + tok, 8 * u, 1.0f, cs);
+      else if (!pass)
+        load_cos_sin<4>(rope, pos0 + tok, 4 * u, 1.0f, cs);
+#pragma unroll
+      for (int h = 0; h < HP; ++h) {
+        if (h0 + h < hq) {
+          if (two) {
+            turn_piece<false, 8>(a[h], b[h], cs);
+            *reinterpret_cast<half8_t*>(y + h * D + d + half) = b[h];
+          } else if (!pass) {
+            turn_piece<true, 4>(a[h], a[h], cs);
+          }
+          *reinterpret_cast<half8_t*>(y + h * D + d) = a[h];
+        }
+      }
+    }
+  } else {
     const int pairs = rope.rot >> 1, units = pairs + D - rope.rot, per = hq * units;
-    for (int e = tid; e < (t1 - t0) * per; e += 256) {
+    for (int e = threadIdx.x; e < (t1 - t0) * per; e += 256) {
       const int tok = t0 + e / per, rest = e % per, h = rest / units, u = rest % units;
       const _Float16* x = qr.p + (int64_t)(q.q0 + tok) * qr.stride + (int64_t)h * D;
       _Float16* y = qo.p + (int64_t)(q.q0 + tok) * qo.stride + (int64_t)h * D;
@@ -77,139 +283,97 @@ __global__ __launch_bounds__(256) void k_append(KvView kv, BatchView b, RowsIn q
         y[rope.rot + u - pairs] = x[rope.rot + u - pairs];
       } else {
         const int i0 = rope.interleaved ? 2 * u : u, i1 = rope.interleaved ? i0 + 1 : u + pairs;
-        const float2 r = turn((float)x[i0], (float)x[i1], cos_sin(rope, (int64_t)q.len - q.n + tok, u));
+        const float2 r = turn((float)x[i0], (float)x[i1], cos_sin(rope, pos0 + tok, u));
         y[i0] = (_Float16)r.x;
         y[i1] = (_Float16)r.y;
       }
     }
+  }
+}
+
+template <int D, int FMT, bool VEC>
+__global__ __launch_bounds__(256) void k_append(KvView kv, BatchView b, RowsIn qr, int hq, RowsIn kr, RowsIn vr,
+                                                RopeView rope, RowsOut qo, int touched, int kv_groups,
+                                                int q_tokens, int q_groups) {
+  const int tid = threadIdx.x;
+  if ((int)blockIdx.x >= kv_groups) {
+    const int w = (int)blockIdx.x - kv_groups;
+    const int s = w / q_groups, t0 = (w % q_groups) * q_tokens;
+    const Seq q = seq_of(b, kv, s);
+    turn_queries<D, VEC>(q, t0, min(q.n, t0 + q_tokens), hq, qr, qo, rope);
     return;
   }
-  __shared__ Tile<D> lk, lv;
-  __shared__ float red[4][2];
-  __shared__ int bad_any;
-  __shared__ uint8_t bad_tok[kKvBlock];
+  __shared__ __attribute__((aligned(16))) Tile<D> tile;
   const int h = (int)blockIdx.x % kv.hk, rest = (int)blockIdx.x / kv.hk, j = rest % touched, s = rest / touched;
   const Seq q = seq_of(b, kv, s);
+  if (q.n == 0) return;
   const int before = q.len - q.n;
   const int first = max(before, 0) / kKvBlock, last_full = q.cap / kKvBlock;   // blocks before last_full are full
-  if (q.n == 0) return;
   const int blk = first + j;
   if (blk < last_full) {
     const int p0 = blk * kKvBlock;
     const int id = b.table[(int64_t)s * b.width + blk];
-    const bool reads_tail = before > p0;
     // a block that cannot be written is dropped; so is one whose earlier tokens have no slot to come from
-    const bool ok = (uint64_t)(int64_t)id < (uint64_t)kv.blocks && (!reads_tail || q.slot >= 0);
-    if (ok) {
-      if (tid == 0) bad_any = 0;
-      if (tid < kKvBlock) bad_tok[tid] = 0;
-      stage<D, true>(lk, kv, q, h, p0, kr, rope);
-      stage<D, false>(lv, kv, q, h, p0, vr, rope);
+    if ((uint64_t)(int64_t)id < (uint64_t)kv.blocks && (before <= p0 || q.slot >= 0)) {
+      stage<D, VEC>(tile, kv, q, h, p0, kr, vr, rope);
       __syncthreads();
-      // a quarter of a key row each, the values by columns: D / 4 elements of both a thread
-      constexpr int E = D / 4;
-      const int kt = tid >> 2, kd = (tid & 3) * E;
-      const int vd = tid / (256 / D), vt = (tid % (256 / D)) * E;   // 64 tokens / (256 / D) = D / 4
-      float ka[E], va[E], km = 0.0f, vm = 0.0f;
-      bool bad = false;
-#pragma unroll
-      for (int i = 0; i < E; ++i) {
-        const _Float16 x = lk.x[kt][kd + i], y = lv.x[vt + i][vd];
-        const bool fx = finite_h(x), fy = finite_h(y);
-        bad |= !fx || !fy;
-        if (!fx) bad_tok[kt] = 1;
-        if (!fy) bad_tok[vt + i] = 1;
-        ka[i] = fx ? (float)x : 0.0f;
-        va[i] = fy ? (float)y : 0.0f;
-        km = fmaxf(km, fabsf(ka[i]));
-        vm = fmaxf(vm, fabsf(va[i]));
-      }
-#pragma unroll
-      for (int d = 32; d > 0; d >>= 1) {
-        km = fmaxf(km, __shfl_xor(km, d));
-        vm = fmaxf(vm, __shfl_xor(vm, d));
-      }
-      if ((tid & 63) == 0) {
-        red[tid >> 6][0] = km;
-        red[tid >> 6][1] = vm;
-      }
-      if (bad) bad_any = 1;
-      __syncthreads();
-      km = fmaxf(fmaxf(red[0][0], red[1][0]), fmaxf(red[2][0], red[3][0]));
-      vm = fmaxf(fmaxf(red[0][1], red[1][1]), fmaxf(red[2][1], red[3][1]));
-      if (bad_any) {   // rare: the key rows of vectors that are not finite count as zeros, as they do from the tail
-        __syncthreads();
-        if (bad_tok[kt]) {
-#pragma unroll
-          for (int i = 0; i < E; ++i) ka[i] = 0.0f;
-        }
-        km = 0.0f;
-#pragma unroll
-        for (int i = 0; i < E; ++i) km = fmaxf(km, fabsf(ka[i]));
-#pragma unroll
-        for (int d = 32; d > 0; d >>= 1) km = fmaxf(km, __shfl_xor(km, d));
-        if ((tid & 63) == 0) red[tid >> 6][0] = km;
-        __syncthreads();
-        km = fmaxf(fmaxf(red[0][0], red[1][0]), fmaxf(red[2][0], red[3][0]));
-      }
-      const float ki = km > 0.0f ? kMax * (1.0f / km) : 0.0f, vi = vm > 0.0f ? kMax * (1.0f / vm) : 0.0f;
-      const int64_t base = ((int64_t)id * kv.hk + h) * kKvBlock * D;
-      uint32_t* ko = reinterpret_cast<uint32_t*>(kv.kc + base + (int64_t)kt * D + kd);
-      uint32_t* vo = reinterpret_cast<uint32_t*>(kv.vc + base + (int64_t)vd * kKvBlock + vt);
-#pragma unroll
-      for (int i = 0; i < E; i += 4) {
-        ko[i / 4] = code4<FMT>(ka[i] * ki, ka[i + 1] * ki, ka[i + 2] * ki, ka[i + 3] * ki);
-        vo[i / 4] = code4<FMT>(va[i] * vi, va[i + 1] * vi, va[i + 2] * vi, va[i + 3] * vi);
-      }
-      if (tid == 0) {
-        // the keys carry the mark of a vector that is not finite: a NaN scale makes the head's
-        // scores NaN for the rows that attend to the block, and masked scores are replaced before use
-        kv.ks[(int64_t)id * kv.hk + h] = bad_any ? __builtin_nanf("") : km / kMax;
-        kv.vs[(int64_t)id * kv.hk + h] = vm / kMax;
-      }
+      code_block<D, FMT>(tile, kv, id, h);
     }
   }
-  // the tokens that stay open
-  if (j != 0 || q.slot < 0) return;
+  // The tokens that stay open: by the workgroup of their block, but after the first block's reads of the tail where it
+  // has any and becomes full, since they may take the same places.
   const int open0 = last_full * kKvBlock, from = max(max(before, 0), open0);
-  if (from >= q.cap) return;
-  __syncthreads();   // the tail's tokens of the first block are in registers or written by now
+  const int owner = before > first * kKvBlock && first < last_full ? 0 : last_full - first;
+  if (j != owner || q.slot < 0 || from >= q.cap) return;
+  __syncthreads();
   const int wave = tid >> 6, lane = tid & 63;
   const int64_t base = ((int64_t)q.slot * kv.hk + h) * kKvBlock * D;
-  for (int p = from + wave; p < q.cap; p += 4) {
-    const int64_t row = q.q0 + p - before;
-    const _Float16* xk = kr.p + row * kr.stride + (int64_t)h * D;
-    const _Float16* xv = vr.p + row * vr.stride + (int64_t)h * D;
-    _Float16 a[D / 64], v[D / 64];
-    bool bad = false;
+  constexpr int E = D / 64, B = 4;   // elements of a lane, tokens a wave has under way at once
+  for (int p0 = from + wave; p0 < q.cap; p0 += 4 * B) {
+    _Float16 a[B][E], v[B][E];
 #pragma unroll
-    for (int i = 0; i < D / 64; ++i) {
-      const int d = lane + 64 * i;
-      a[i] = rope.table ? turned(xk, d, rope, p) : xk[d];
-      v[i] = xv[d];
-      bad |= !finite_h(a[i]) || !finite_h(v[i]);
+    for (int t = 0; t < B; ++t) {
+      const int p = min(p0 + 4 * t, q.cap - 1);
+      const int64_t row = q.q0 + p - before;
+      const _Float16* xk = kr.p + row * kr.stride + (int64_t)h * D;
+      const _Float16* xv = vr.p + row * vr.stride + (int64_t)h * D;
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        const int d = lane + 64 * i;
+        a[t][i] = rope.table ? turned(xk, d, rope, p) : xk[d];
+        v[t][i] = xv[d];
+      }
     }
-    // a vector that is not finite: the key row is NaN as a whole (its scores are NaN, and only its),
-    // the value column holds zeros in its place, so that a masked token multiplies nothing but numbers
-    const bool any = __any(bad);
 #pragma unroll
-    for (int i = 0; i < D / 64; ++i) {
-      const int d = lane + 64 * i;
-      kv.kt[base + (int64_t)(p - open0) * D + d] = any ? (_Float16)__builtin_nanf("") : a[i];
-      kv.vt[base + (int64_t)d * kKvBlock + (p - open0)] = finite_h(v[i]) ? v[i] : (_Float16)0.0f;
+    for (int t = 0; t < B; ++t) {
+      const int p = p0 + 4 * t;
+      if (p >= q.cap) break;
+      bool bad = false;
+#pragma unroll
+      for (int i = 0; i < E; ++i) bad |= !finite_h(a[t][i]) || !finite_h(v[t][i]);
+      // a vector that is not finite: the key row is NaN as a whole (its scores are NaN, and only its),
+      // the value column holds zeros in its place, so that a masked token multiplies nothing but numbers
+      const bool any = __any(bad);
+#pragma unroll
+      for (int i = 0; i < E; ++i) {
+        const int d = lane + 64 * i;
+        kv.kt[base + (int64_t)(p - open0) * D + d] = any ? (_Float16)__builtin_nanf("") : a[t][i];
+        kv.vt[base + (int64_t)d * kKvBlock + (p - open0)] = finite_h(v[t][i]) ? v[t][i] : (_Float16)0.0f;
+      }
     }
   }
 }
 
-template <int D>
-hipError_t go(const KvView& kv, int format, const BatchView& b, RowsIn q, int hq, RowsIn k, RowsIn v,
-              const RopeView& rope, RowsOut qo, int touched, int kv_groups, int q_tokens, int q_groups, int groups,
-              hipStream_t s) {
+template <int D, int FMT>
+hipError_t go(const KvView& kv, const BatchView& b, RowsIn q, int hq, RowsIn k, RowsIn v, const RopeView& rope,
+              RowsOut qo, int touched, int kv_groups, int q_tokens, int q_groups, int groups, hipStream_t s) {
   const dim3 g((unsigned)groups), t(256);
-  if (format == MQ_KV_INT8)
-    k_append<D, MQ_KV_INT8><<<g, t, 0, s>>>(kv, b, q, hq, k, v, rope, qo, touched, kv_groups, q_tokens, q_groups);
+  const bool vec = wide_rows(k.p, k.stride) && wide_rows(v.p, v.stride) && (!rope.table || piecewise(rope)) &&
+                   (q_groups == 0 || (wide_rows(q.p, q.stride) && wide_rows(qo.p, qo.stride)));
+  if (vec)
+    k_append<D, FMT, true><<<g, t, 0, s>>>(kv, b, q, hq, k, v, rope, qo, touched, kv_groups, q_tokens, q_groups);
   else
-    k_append<D, MQ_KV_E4M3><<<g, t, 0, s>>>(kv, b, q, hq, k, v, rope, qo, touched, kv_groups, q_tokens, q_groups);
+    k_append<D, FMT, false><<<g, t, 0, s>>>(kv, b, q, hq, k, v, rope, qo, touched, kv_groups, q_tokens, q_groups);
   return hipGetLastError();
 }
 
@@ -230,10 +394,16 @@ hipError_t launch_kv_append(const KvView& kv, int dim, int format, const BatchVi
     *grid_too_large = true;
     return hipSuccess;
   }
-  return dim == 64 ? go<64>(kv, format, b, q, hq, k, v, rope, qo, (int)touched, (int)kv_groups, (int)q_tokens,
-                            (int)q_groups, (int)groups, s)
-                   : go<128>(kv, format, b, q, hq, k, v, rope, qo, (int)touched, (int)kv_groups, (int)q_tokens,
-                             (int)q_groups, (int)groups, s);
+  const auto run = [&](auto d, auto f) {
+    return go<decltype(d)::value, decltype(f)::value>(kv, b, q, hq, k, v, rope, qo, (int)touched, (int)kv_groups,
+                                                      (int)q_tokens, (int)q_groups, (int)groups, s);
+  };
+  using std::integral_constant;
+  if (dim == 64)
+    return format == MQ_KV_INT8 ? run(integral_constant<int, 64>{}, integral_constant<int, MQ_KV_INT8>{})
+                                : run(integral_constant<int, 64>{}, integral_constant<int, MQ_KV_E4M3>{});
+  return format == MQ_KV_INT8 ? run(integral_constant<int, 128>{}, integral_constant<int, MQ_KV_INT8>{})
+                              : run(integral_constant<int, 128>{}, integral_constant<int, MQ_KV_E4M3>{});
 }
 
 }  // namespace mq

@@ -91,35 +91,12 @@ __global__ __launch_bounds__(256) void k_rope_vec(const _Float16* x, uint32_t n,
       if (!INTER) b[h] = *reinterpret_cast<const half8_t*>(xr + h * xh + 8 * u + half);
     }
   }
-  const int64_t p = pos[t];
   float2 cs[NP];
-  if ((uint64_t)p < (uint64_t)rope.positions) {
-    const float4* row4 = reinterpret_cast<const float4*>(rope.table + p * half + NP * u);   // 16-byte aligned: half and NP u are even
-#pragma unroll
-    for (int i = 0; i < NP / 2; ++i) {
-      const float4 f = row4[i];
-      cs[2 * i] = make_float2(f.x, f.y * dir);
-      cs[2 * i + 1] = make_float2(f.z, f.w * dir);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < NP; ++i) cs[i] = make_float2(__builtin_nanf(""), __builtin_nanf(""));
-  }
+  load_cos_sin<NP>(rope, pos[t], NP * u, dir, cs);
 #pragma unroll
   for (int h = 0; h < HP; ++h) {
     if (h0 + h < heads) {
-#pragma unroll
-      for (int i = 0; i < NP; ++i) {
-        const float2 r = INTER ? turn((float)a[h][2 * i], (float)a[h][2 * i + 1], cs[i])
-                               : turn((float)a[h][i], (float)b[h][i], cs[i]);
-        if (INTER) {
-          a[h][2 * i] = (_Float16)r.x;
-          a[h][2 * i + 1] = (_Float16)r.y;
-        } else {
-          a[h][i] = (_Float16)r.x;
-          b[h][i] = (_Float16)r.y;
-        }
-      }
+      turn_piece<INTER, NP>(a[h], b[h], cs);
       *reinterpret_cast<half8_t*>(yr + h * yh + 8 * u) = a[h];
       if (!INTER) *reinterpret_cast<half8_t*>(yr + h * yh + 8 * u + half) = b[h];
     }
@@ -145,16 +122,13 @@ hipError_t launch_rope(const _Float16* x, int64_t tokens, int heads, int dim, in
   const float dir = inverse ? -1.0f : 1.0f;
   const bool inter = rope.interleaved != 0;
   const int piece = inter ? 8 : 16;   // rotated elements of a unit
-  const auto wide = [](const void* p, int64_t a, int64_t b) {
-    return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && a % 8 == 0 && b % 8 == 0;
-  };
   const int units = rope.rot / piece + (dim - rope.rot) / 8;
   // heads of a thread: 4 once that still leaves the GPU full (256 CUs of 1024 threads), else 1
   const int64_t one = tokens * heads * units;
   const int hp = one >= 4 * 262144 ? 4 : 1;
   const int64_t n = tokens * ((heads + hp - 1) / hp) * units;
-  if (rope.rot % piece == 0 && dim % 8 == 0 && wide(x, xt, xh) && wide(y, yt, yh) &&
-      (reinterpret_cast<uintptr_t>(rope.table) & 15u) == 0 && n < (int64_t(1) << 31)) {
+  if (piecewise(rope) && dim % 8 == 0 && wide_rows(x, xt) && xh % 8 == 0 && wide_rows(y, yt) && yh % 8 == 0 &&
+      n < (int64_t(1) << 31)) {
     const dim3 g((unsigned)((n + 255) / 256)), b(256);
     const uint32_t un = (uint32_t)n, uu = (uint32_t)units;
     if (inter) {
