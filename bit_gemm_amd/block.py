@@ -80,26 +80,33 @@ lib = _load()
 _F16 = torch.float16
 
 
-def _stream(stream) -> int:
+def _current_stream(index: int) -> int:
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+# the current stream's handle without the Python object around it, where torch has that (3 us less a call)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _current_stream)
+
+
+def _stream(stream, t) -> int:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream(t.get_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _rows(t, name: str, heads=None, dim=None):
-    """Checks an fp16 [tokens, heads, dim] GPU tensor whose rows are dense."""
+    """Checks an fp16 [tokens, heads, dim] GPU tensor whose heads lie dense in a
+    row; gives its tokens, heads and the elements between rows (of at most one
+    row: its own width, whatever its stride says)."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype is not _F16:
         raise TypeError(f"{name} must be a float16 tensor on the GPU")
     if t.dim() != 3 or (heads is not None and t.shape[1] != heads) or (dim is not None and t.shape[2] != dim):
         raise ValueError(f"{name} must be [tokens, {heads or 'heads'}, {dim or 'head dim'}]")
-    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2]):
+    T, H, D = t.shape
+    st, sh, sd = t.stride()
+    if (sd != 1 and D > 1) or (H > 1 and sh != D):
         raise ValueError(f"the heads of a row of {name} must be dense")
-    return t
-
-
-def _row_stride(t) -> int:
-    """Elements between rows; for at most one row any stride stands, so the row's own width."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+    return T, H, st if T > 1 else H * D
 
 
 def _ints(t, name: str, shape):
@@ -124,8 +131,8 @@ class Rope:
         spec = _RopeSpec(self.rot_dim, SCALINGS[scaling], theta, factor, original, turns_fast, turns_slow)
         self.table = torch.empty((max(self.positions, 1), max(self.rot_dim // 2, 1), 2), dtype=torch.float32,
                                  device="cuda")
-        _check(lib.mq_rope_table(ctypes.byref(spec), self.positions, self.table.data_ptr(), _stream(stream)),
-               "mq_rope_table")
+        _check(lib.mq_rope_table(ctypes.byref(spec), self.positions, self.table.data_ptr(),
+                                 _stream(stream, self.table)), "mq_rope_table")
         self._plan = _RopePlan(self.table.data_ptr(), self.positions, self.rot_dim, LAYOUTS[layout])
         self._ref = ctypes.addressof(self._plan)
 
@@ -141,11 +148,15 @@ def mq_rope(x, rope: Rope, pos, inverse: bool = False, out=None, stream=None):
     T, H, D = x.shape
     _ints(pos, "pos", (T,))
     if out is None:
-        out = torch.empty((T, H, D), dtype=_F16, device=x.device)
+        out = x.new_empty((T, H, D))
     elif out.dtype is not _F16 or not out.is_cuda or out.shape != x.shape or out.stride(2) != 1:
         raise ValueError("out must be a float16 GPU tensor of x's shape with dense heads")
-    _check(lib.mq_rope(x.data_ptr(), T, H, D, x.stride(0), x.stride(1), pos.data_ptr(), rope._ref, int(inverse),
-                       out.data_ptr(), out.stride(0), out.stride(1), _stream(stream)), "mq_rope")
+    xt, xh, _ = x.stride()
+    yt, yh, _ = out.stride()
+    code = lib.mq_rope(x.data_ptr(), T, H, D, xt, xh, pos.data_ptr(), rope._ref, int(inverse), out.data_ptr(), yt, yh,
+                       _stream(stream, x))
+    if code:
+        raise MQError(code, "mq_rope")
     return out
 
 
@@ -223,28 +234,28 @@ def mq_kv_append(q, k, v, cache: KVCache, batch: KVBatch, rope: Rope | None = No
     as it is. Rows may lie apart (slices of a joined projection). Enqueued on
     `stream` (no sync)."""
     D, hk = cache.head_dim, cache.kv_heads
-    _rows(k, "k", hk, D)
-    _rows(v, "v", hk, D)
-    T = k.shape[0]
-    if v.shape[0] != T:
+    T, _, ks = _rows(k, "k", hk, D)
+    Tv, _, vs = _rows(v, "v", hk, D)
+    if Tv != T:
         raise ValueError("k and v must have the same tokens")
-    qp = qo = None
+    qp = qo = rp = None
     heads = qs = qos = 0
-    if rope is not None and q is not None:
-        _rows(q, "q", None, D)
-        heads = q.shape[1]
-        if q_out is None:
-            q_out = torch.empty((T, heads, D), dtype=_F16, device=q.device)
-        else:
-            _rows(q_out, "q_out", heads, D)
-        if q.shape[0] != T or q_out.shape[0] != T:
-            raise ValueError("q, k and v must have the same tokens")
-        qp, qo, qs, qos = q.data_ptr(), q_out.data_ptr(), _row_stride(q), _row_stride(q_out)
-    if T == 0:
-        return q if qo is None else q_out
-    _check(lib.mq_kv_append(cache._ref, batch._with(T), qp, heads, qs, k.data_ptr(), _row_stride(k), v.data_ptr(),
-                            _row_stride(v), None if rope is None else rope._ref, qo, qos, _stream(stream)),
-           "mq_kv_append")
+    if rope is not None:
+        rp = rope._ref
+        if q is not None:
+            Tq, heads, qs = _rows(q, "q", None, D)
+            if q_out is None:
+                q_out, To, qos = q.new_empty((Tq, heads, D)), Tq, heads * D
+            else:
+                To, _, qos = _rows(q_out, "q_out", heads, D)
+            if Tq != T or To != T:
+                raise ValueError("q, q_out, k and v must have the same tokens")
+            qp, qo = q.data_ptr(), q_out.data_ptr()
+    if T:
+        code = lib.mq_kv_append(cache._ref, batch._with(T), qp, heads, qs, k.data_ptr(), ks, v.data_ptr(), vs, rp, qo,
+                                qos, _stream(stream, k))
+        if code:
+            raise MQError(code, "mq_kv_append")
     return q if qo is None else q_out
 
 
@@ -268,30 +279,49 @@ def mq_kv_attention(q, cache: KVCache, batch: KVBatch, causal: bool = True, scal
     at least kv_attention_workspace bytes (None: taken from torch's allocator).
     Enqueued on `stream` (no sync)."""
     D = cache.head_dim
-    _rows(q, "q", None, D)
-    T, H = q.shape[0], q.shape[1]
+    T, H, qs = _rows(q, "q", None, D)
     if out is None:
-        out = torch.empty((T, H, D), dtype=_F16, device=q.device)
+        out, os_ = q.new_empty((T, H, D)), H * D
     else:
-        _rows(out, "out", H, D)
-        if out.shape[0] != T:
+        To, _, os_ = _rows(out, "out", H, D)
+        if To != T:
             raise ValueError("out must have q's tokens")
     if T == 0:
         return out
     need = kv_attention_workspace(cache, batch, T, H)
-    if workspace is None:
-        ws = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
-        if ws is not None and stream is not None:   # its memory is not given out again before the kernels are done
-            ws.record_stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
-    else:
+    wp, nw = None, 0
+    if workspace is not None:
         if workspace.dtype is not torch.uint8 or not workspace.is_cuda or not workspace.is_contiguous():
             raise TypeError("workspace must be a contiguous uint8 tensor on the GPU")
-        ws = workspace
-    _check(lib.mq_kv_attention(cache._ref, batch._with(T), q.data_ptr(), H, _row_stride(q), int(causal),
-                               D ** -0.5 if scale is None else scale, out.data_ptr(), _row_stride(out),
-                               None if ws is None else ws.data_ptr(), 0 if ws is None else ws.numel(),
-                               _stream(stream)), "mq_kv_attention")
+        wp, nw = workspace.data_ptr(), workspace.numel()
+    elif need:
+        ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+        if stream is not None:   # its memory is not given out again before the kernels are done
+            ws.record_stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
+        wp, nw = ws.data_ptr(), need
+    code = lib.mq_kv_attention(cache._ref, batch._with(T), q.data_ptr(), H, qs, int(causal),
+                               D ** -0.5 if scale is None else scale, out.data_ptr(), os_, wp, nw, _stream(stream, q))
+    if code:
+        raise MQError(code, "mq_kv_attention")
     return out
+
+
+def _matrix(t, name: str, dt, shape):
+    """Address and row stride of a [tokens, width] GPU tensor with dense rows."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype is not dt:
+        raise TypeError(f"{name} must be a {dt} tensor on the GPU")
+    st = t.stride()
+    if t.shape != shape or st[1] != 1:
+        raise ValueError(f"{name} must be {list(shape)} with dense rows")
+    return t.data_ptr(), st[0] if shape[0] > 1 else shape[1]
+
+
+def _vector(t, name: str, width: int):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype is not _F16 or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous float16 tensor on the GPU")
+    if t.dim() != 1 or t.shape[0] != width:
+        raise ValueError(f"{name} must be [{width}]")
+    return t.data_ptr()
 
 
 def mq_norm_residual(y, r, w_pre, w_post=None, gate=None, alpha: float = 1.0, beta: float = 1.0, eps: float = 1e-6,
@@ -306,47 +336,40 @@ def mq_norm_residual(y, r, w_pre, w_post=None, gate=None, alpha: float = 1.0, be
         raise TypeError("r must be a float16 or float32 tensor on the GPU")
     if r.dim() != 2 or r.stride(1) != 1:
         raise ValueError("r must be [tokens, width] with dense rows")
-    M, W = r.shape
-
-    def mat(t, name, dt):
-        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype is not dt:
-            raise TypeError(f"{name} must be a {dt} tensor on the GPU")
-        if t.shape != r.shape or t.stride(1) != 1:
-            raise ValueError(f"{name} must be [{M}, {W}] with dense rows")
-        return t.data_ptr(), t.stride(0) if M > 1 else W
-
-    def vec(t, name):
-        if t is None:
-            return None
-        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype is not _F16 or not t.is_contiguous():
-            raise TypeError(f"{name} must be a contiguous float16 tensor on the GPU")
-        if t.dim() != 1 or t.shape[0] != W:
-            raise ValueError(f"{name} must be [{W}]")
-        return t.data_ptr()
-
-    yp = gp = rp = hp = None
+    shape, dt = r.shape, r.dtype
+    M, W = shape
+    yp = gp = rp = hp = wpost = wpre = None
     ys = gs = rs = hs = 0
     if y is not None:
-        yp, ys = mat(y, "y", _F16)
+        yp, ys = _matrix(y, "y", _F16, shape)
         if r_out is None:
-            r_out = torch.empty((M, W), dtype=r.dtype, device=r.device)
-        rp, rs = mat(r_out, "r_out", r.dtype)
+            r_out = r.new_empty(shape)
+            rp, rs = r_out.data_ptr(), W
+        else:
+            rp, rs = _matrix(r_out, "r_out", dt, shape)
+        if w_post is not None:
+            wpost = _vector(w_post, "w_post", W)
         if gate is not None:
             if gate.dim() == 1:
-                gp = vec(gate, "gate")
+                gp = _vector(gate, "gate", W)
             else:
-                gp, gs = mat(gate, "gate", _F16)
+                gp, gs = _matrix(gate, "gate", _F16, shape)
     else:
         r_out = r
     if w_pre is not None:
+        wpre = _vector(w_pre, "w_pre", W)
         if h_out is None:
-            h_out = torch.empty((M, W), dtype=_F16, device=r.device)
-        hp, hs = mat(h_out, "h_out", _F16)
+            h_out = w_pre.new_empty(shape)
+            hp, hs = h_out.data_ptr(), W
+        else:
+            hp, hs = _matrix(h_out, "h_out", _F16, shape)
     else:
         h_out = None
     if M == 0:
         return r_out, h_out
-    a = _NormArgs(yp, r.data_ptr(), gp, vec(w_post, "w_post") if yp else None, vec(w_pre, "w_pre"), rp, hp, M, W, ys,
-                  r.stride(0) if M > 1 else W, gs, rs, hs, alpha, beta, eps, weight_offset, r.dtype is torch.float32)
-    _check(lib.mq_norm_residual(ctypes.byref(a), _stream(stream)), "mq_norm_residual")
+    a = _NormArgs(yp, r.data_ptr(), gp, wpost, wpre, rp, hp, M, W, ys, r.stride(0) if M > 1 else W, gs, rs, hs, alpha,
+                  beta, eps, weight_offset, dt is torch.float32)
+    code = lib.mq_norm_residual(ctypes.addressof(a), _stream(stream, r))
+    if code:
+        raise MQError(code, "mq_norm_residual")
     return r_out, h_out
