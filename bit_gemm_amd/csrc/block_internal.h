@@ -53,11 +53,15 @@ hipError_t launch_rope(const _Float16* x, int64_t tokens, int heads, int dim, in
 hipError_t launch_kv_append(const KvView& kv, int dim, int format, const BatchView& b, RowsIn q, int hq, RowsIn k,
                             RowsIn v, const RopeView& rope, RowsOut qo, bool* grid_too_large, hipStream_t s);
 
-constexpr int kAttnRows = 256;   // query rows a workgroup of the kernel for many rows holds
+// Query rows a workgroup of the kernel for many rows holds: 32 a wave, 8 waves, and one workgroup a CU; for heads of 64
+// elements 4 waves and two workgroups a CU, which even out better (5 pieces: 105 us against 115; with heads of 128 the
+// codes laid twice as often cost more: a prompt of 4096 164 us against 150).
+constexpr int attn_rows(int dim) { return dim == 64 ? 128 : 256; }
+
 
 // How the attention of a batch is run: a rule on sizes alone (kv_attn.hip).
 struct AttnPlan {
-  int nt;             // blocks of 16 query rows a workgroup holds; 0: the kernel for many rows, kAttnRows of them
+  int nt;             // blocks of 16 query rows a workgroup holds; 0: the kernel for many rows, attn_rows of them
   int row_tiles;      // workgroups along the rows of the longest sequence
   int chunk;          // cache blocks of one workgroup
   int splits;         // workgroups along the cache of the longest sequence; 1: no workspace

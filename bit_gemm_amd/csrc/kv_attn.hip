@@ -340,10 +340,10 @@ hipError_t go(const AttnArgs& A, const AttnPlan& p, hipStream_t s) {
   if (p.nt == 0) {
     e = launch_attn_rows(A, D, FMT, p, s);
   } else {
-    switch (p.nt) {
-      case 1: k_attn_split<D, FMT, 1><<<g, ts, 0, s>>>(A); break;
-      case 2: k_attn_split<D, FMT, 2><<<g, ts, 0, s>>>(A); break;
-      default: k_attn_split<D, FMT, 4><<<g, ts, 0, s>>>(A); break;
+    if (p.nt == 1) k_attn_split<D, FMT, 1><<<g, ts, 0, s>>>(A);
+    if (p.nt == 2) k_attn_split<D, FMT, 2><<<g, ts, 0, s>>>(A);
+    if constexpr (D == 64) {
+      if (p.nt == 4) k_attn_split<D, FMT, 4><<<g, ts, 0, s>>>(A);
     }
     e = hipGetLastError();
   }
@@ -364,7 +364,10 @@ AttnPlan plan_attention(int hk, int hq, int dim, int64_t seqs, int64_t tokens, i
   if (max_new > tokens && tokens > 0) max_new = tokens;
   const int64_t rows = max_new * (hq / hk), blocks = up(max_len, kKvBlock);
   int64_t one, splits;
-  if (rows <= 64) {
+  // Up to 32 rows of 128 elements (64 of 64) run on the kernel for few rows, whatever their number of blocks; beyond
+  // that it was slower: 64 rows of 128 took 32.8 us against 26.9 (8 sequences of 3000 tokens), 60 rows of 60 tokens 16.8
+  // against 7.5; 64 rows of 64 elements 18.5 against 24.3.
+  if (rows <= (dim == 64 ? 64 : 32)) {
     p.nt = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
     // split the cache until every CU has a workgroup, but leave a wave two blocks: 512 and 1024 workgroups read 2 to 20 %
     // slower (1 x 30000, 2 x 65500, 4 x 8000 tokens), with fewer blocks a wave to overlap and more to join
@@ -372,12 +375,16 @@ AttnPlan plan_attention(int hk, int hq, int dim, int64_t seqs, int64_t tokens, i
     one = seqs * p.row_tiles * hk;
     splits = one > 0 ? std::min(up(256, one), up(blocks, 2 * kWaves)) : 1;
   } else {
-    // split the cache, 16 blocks at least a part, until there are about two workgroups a CU (as far as
-    // the host can tell: the tokens give the row tiles that there are, where sequences differ in length)
-    p.row_tiles = (int)up(rows, kAttnRows);
+    // Workgroups before any split, as far as the host can tell: the tokens give the row tiles that there are, where
+    // sequences differ in length. While they leave half of the places on the GPU idle the cache is split to fill them
+    // once, in parts of 4 blocks at least; else, to even out, to fill them about twice, in parts of 16.
+    const int64_t tile = attn_rows(dim), places = 256 * 256 / tile;
+    p.row_tiles = (int)up(rows, tile);
     one = seqs * p.row_tiles * hk;
-    const int64_t tiles = std::min(seqs * p.row_tiles, tokens * (hq / hk) / kAttnRows + seqs);
-    splits = one > 0 ? std::min(up(512, tiles * hk), up(blocks, 16)) : 1;
+    const int64_t there = std::min(seqs * p.row_tiles, tokens * (hq / hk) / tile + seqs) * hk;
+    splits = one <= 0                                  ? 1
+             : 2 * there <= places && blocks >= 16 ? std::min(places / there, up(blocks, 4))
+                                                       : std::min(up(2 * places, there), up(blocks, 16));
   }
   if (splits > 256) splits = 256;
   p.chunk = (int)up(blocks, splits);

@@ -1,7 +1,7 @@
 // Attention over the 8-bit key/value cache for many query rows: prompts and
 // their pieces (kv_attn.hip holds the kernel for few rows and the join).
 //
-// A workgroup of 8 waves holds 256 rows of one kv head (row r = new token
+// A workgroup of 8 waves (heads of 64: of 4) holds 32 rows a wave of one kv head (row r = new token
 // r / g, query head r % g, so the g heads that share the keys share the
 // tile) and walks the 64-token blocks they see. A block's codes are loaded
 // two blocks ahead into registers, widened once for the workgroup and laid
@@ -47,7 +47,6 @@ __device__ __forceinline__ float sum_halves(float v) {
   return __builtin_bit_cast(float, (uint32_t)r.x) + __builtin_bit_cast(float, (uint32_t)r.y);
 }
 
-constexpr int kWaves = kAttnRows / 32;
 constexpr float kSlack = 8.0f;       // how far (powers of two) the maximum may run ahead of the reference
 
 // The swizzle of a key row and of a value row: 16-byte piece -> place. Keys of
@@ -70,7 +69,8 @@ __device__ __forceinline__ void phase_barrier() {
 }
 
 template <int D, int FMT>
-__global__ __launch_bounds__(64 * kWaves, 2) void k_attn_rows(AttnArgs A) {
+__global__ __launch_bounds__(2 * attn_rows(D), 2) void k_attn_rows(AttnArgs A) {
+  constexpr int kWaves = attn_rows(D) / 32;
   constexpr int THREADS = 64 * kWaves, KS = D / 16, DT = D / 32;
   constexpr int PIECES = kKvBlock * D / 16;               // 16-byte pieces of codes of a block's keys (and values)
   constexpr int LOADS = (2 * PIECES + THREADS - 1) / THREADS;
@@ -372,7 +372,7 @@ __global__ __launch_bounds__(64 * kWaves, 2) void k_attn_rows(AttnArgs A) {
 }  // namespace
 
 hipError_t launch_attn_rows(const AttnArgs& A, int dim, int format, const AttnPlan& p, hipStream_t s) {
-  const dim3 g((unsigned)p.groups), t(64 * kWaves);
+  const dim3 g((unsigned)p.groups), t(2 * attn_rows(dim));
   if (dim == 64) {
     if (format == MQ_KV_INT8) k_attn_rows<64, MQ_KV_INT8><<<g, t, 0, s>>>(A);
     else k_attn_rows<64, MQ_KV_E4M3><<<g, t, 0, s>>>(A);
