@@ -17,8 +17,8 @@
 // values). A block's scales stay in fp32: with t = (k scale) s + log2(v scale)
 // the weights are p = 2^(t - m), so that O sums codes in units of 2^-m and no
 // block needs its own accumulator; the softmax's sum takes p / (v scale). p is
-// rounded to fp16 (relative 2^-11), and the sum, in fp32, takes the rounded values:
-// where few tokens weigh, the roundings cancel. All else is fp32.
+// rounded to fp16 (relative 2^-11); its sum is not, since a block of small values
+// has small p whatever its scores. All else is fp32.
 //
 // Bound by HBM: 2 head_dim bytes for each cached token and kv head. A wave's
 // loads are never conditional and keys of its next block are requested as soon
@@ -113,7 +113,6 @@ __global__ __launch_bounds__(64 * kWaves, NT == 4 ? 1 : 2) void k_attn_split(Att
 
   float4_t o[NT][DT];
   float m[NT], l[NT];
-  const float one = opaque_one();
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     m[t] = kNoMax;
@@ -148,12 +147,10 @@ __global__ __launch_bounds__(64 * kWaves, NT == 4 ? 1 : 2) void k_attn_split(Att
       }
       float sum = 0.0f;
 #pragma unroll
-      for (int i = 0; i < 16; i += 2) {
-        const half2_t e = round_pair(__builtin_amdgcn_exp2f(p[i] - m[t]), __builtin_amdgcn_exp2f(p[i + 1] - m[t]));
-        sum = fmaf((float)e.x, one, sum);
-        sum = fmaf((float)e.y, one, sum);
-        pf[t][i >> 3][i & 7] = e.x;
-        pf[t][i >> 3][(i & 7) + 1] = e.y;
+      for (int i = 0; i < 16; ++i) {
+        const float e = __builtin_amdgcn_exp2f(p[i] - m[t]);
+        sum += e;
+        pf[t][i >> 3][i & 7] = (_Float16)e;
       }
       l[t] = fmaf(sum, __builtin_amdgcn_rcpf(vs), l[t]);
     }

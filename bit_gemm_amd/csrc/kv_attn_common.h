@@ -29,21 +29,6 @@ __device__ __forceinline__ half8_t widen8(uint32_t a, uint32_t b) {
   return __builtin_bit_cast(half8_t, r);
 }
 
-// 1, kept from the compiler: fmaf((float)half, one, sum) then stays one mixed-precision instruction.
-__device__ __forceinline__ float opaque_one() {
-  float one = 1.0f;
-  asm("" : "+v"(one));
-  return one;
-}
-
-// Two weights as fp16, in one register: kept so from the compiler, which would convert them apart for the sum.
-__device__ __forceinline__ half2_t round_pair(float a, float b) {
-  const half2_t p = {(_Float16)a, (_Float16)b};
-  uint32_t u = __builtin_bit_cast(uint32_t, p);
-  asm("" : "+v"(u));
-  return __builtin_bit_cast(half2_t, u);
-}
-
 struct AttnArgs {
   KvView kv;
   BatchView b;

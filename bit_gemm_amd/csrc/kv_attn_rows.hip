@@ -16,8 +16,8 @@
 // needs its own accumulator; the softmax's sum takes p / (v scale). The
 // reference m follows the running maximum only when that has grown by more
 // than 2^8 (p then reaches 2^8 at most, far inside fp16), so the sums are
-// rarely rescaled. p is rounded to fp16 (relative 2^-11), and the sum, in fp32,
-// takes the rounded values: where few tokens weigh, the roundings cancel.
+// rarely rescaled. p is rounded to fp16 (relative 2^-11); its sum is not, since a
+// block of small values has small p whatever its scores.
 // LDS rows are swizzled by 16-byte pieces, so that lanes that read together hit
 // different banks.
 // Bound by the matrix cores and the exponentials beside them.
@@ -143,7 +143,6 @@ __global__ __launch_bounds__(2 * attn_rows(D), 2) void k_attn_rows(AttnArgs A) {
 #pragma unroll
     for (int i = 0; i < 16; ++i) o[d][i] = 0.0f;
   float m = kNoMax, l = 0.0f;
-  const float one = opaque_one();
 
   const int n = max(b1 - b0, 0);
   // Lays stage t into LDS (keys of block t + 1, values of block t): coded blocks only (FAST), or whatever the blocks are.
@@ -253,10 +252,10 @@ __global__ __launch_bounds__(2 * attn_rows(D), 2) void k_attn_rows(AttnArgs A) {
       float sum = 0.0f;
 #pragma unroll
       for (int i = 0; i < 32; ++i) {
-        _Float16 p = (_Float16)__builtin_amdgcn_exp2f(fmaf(sa.t[i >> 4][i & 15], mul, off));
-        if (16 * (i >> 3) + (i & 7) >= left) p = (_Float16)0.0f;   // again: a masked score times a NaN or zero scale is no weight
-        sum = fmaf((float)p, one, sum);
-        pf[i >> 4][(i >> 3) & 1][i & 7] = p;
+        float p = __builtin_amdgcn_exp2f(fmaf(sa.t[i >> 4][i & 15], mul, off));
+        if (16 * (i >> 3) + (i & 7) >= left) p = 0.0f;   // again: a masked score times a NaN or zero scale is no weight
+        sum += p;
+        pf[i >> 4][(i >> 3) & 1][i & 7] = (_Float16)p;
       }
       l = fmaf(sum, __builtin_amdgcn_rcpf(v1), l);
       multiply_values(lv[X]);
@@ -299,13 +298,10 @@ __global__ __launch_bounds__(2 * attn_rows(D), 2) void k_attn_rows(AttnArgs A) {
     multiply_keys(next, lk[X ^ 1]);
     float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int i = 0; i < 32; i += 2) {
-      const half2_t p = round_pair(__builtin_amdgcn_exp2f(fmaf(now.t[i >> 4][i & 15], mul, off)),
-                                   __builtin_amdgcn_exp2f(fmaf(now.t[i >> 4][(i & 15) + 1], mul, off)));
-      sum[i & 2] = fmaf((float)p.x, one, sum[i & 2]);
-      sum[(i & 2) + 1] = fmaf((float)p.y, one, sum[(i & 2) + 1]);
-      pf[i >> 4][(i >> 3) & 1][i & 7] = p.x;
-      pf[i >> 4][(i >> 3) & 1][(i & 7) + 1] = p.y;
+    for (int i = 0; i < 32; ++i) {
+      const float p = __builtin_amdgcn_exp2f(fmaf(now.t[i >> 4][i & 15], mul, off));
+      sum[i & 3] += p;
+      pf[i >> 4][(i >> 3) & 1][i & 7] = (_Float16)p;
     }
     l = fmaf((sum[0] + sum[1]) + (sum[2] + sum[3]), __builtin_amdgcn_rcpf(v1), l);
     multiply_values(lv[X]);

@@ -370,6 +370,64 @@ def test_attention(bk, new, lens, hq, hk, D, causal, fmt):
     check_attention(st, q, new, causal)
 
 
+PIECES = [  # many rows: new tokens, lengths, query heads, kv heads, dim, causal; rows that are checked
+    ([700], [700], 4, 1, 128, True),
+    ([513, 7], [2600, 90], 8, 2, 64, True),
+    ([300], [5000], 2, 2, 128, False),                  # the cache split over workgroups
+    ([64, 400, 129], [64, 464, 3000], 4, 2, 128, True),
+    ([1000], [1024], 1, 1, 64, True),
+]
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("new,lens,hq,hk,D,causal", PIECES)
+def test_attention_of_long_pieces(bk, new, lens, hq, hk, D, causal, fmt):
+    print("pieces", new, lens, hq, hk, D, causal, fmt, flush=True)
+    st = Setup(bk, lens, hk, D, fmt, seed=sum(new) + D)
+    st.fill()
+    q = dev((st.g.standard_normal((sum(new), hq, D)) * 1.5).astype(np.float16))
+    rows = sorted({0, 1, 31, 32, 62, 63, 64, 65, 127, 128, 129, 255, 256, 299, 300, 399, 511, 512, 640, 698, 699, 999})
+    check_attention(st, q, new, causal, rows=rows)
+
+
+@pytest.mark.parametrize("new,hq", [([2], 4), ([90], 4)])
+def test_attention_of_blocks_with_very_different_scales(bk, new, hq):
+    """Values of a block that are all zero, or a thousand times another's; keys likewise; negative and zero scales of
+    the scores: nothing is lost between blocks."""
+    for fmt in ("int8", "e4m3"):
+        st = Setup(bk, [500], 1, 128, fmt, seed=11)
+
+        def values(s, k, v):
+            v[64:128] = 0
+            v[128:192] *= np.float16(1e-3)
+            v[192:256] *= np.float16(1e3)
+            k[128:256] *= np.float16(1e-2)
+            k[256:320] = 0
+            v[320:384] *= np.float16(2e-4)
+        st.fill(values)
+        q = dev(st.g.standard_normal((new[0], hq, 128)).astype(np.float16))
+        rows = [0, 1, 40, 63, 89]
+        for scale in (128 ** -0.5, -0.5, 0.0):
+            check_attention(st, q, new, True, scale=scale, what=f"{fmt} scale {scale}", rows=rows)
+
+
+@pytest.mark.parametrize("new,lens,D", [([1, 1], [2000, 70], 128), ([90, 40], [1500, 700], 64), ([100], [3000], 128)])
+def test_attention_does_not_depend_on_the_bounds(bk, new, lens, D):
+    """max_new and max_len choose how the work is split, not what it gives; the same call gives the same bits."""
+    import torch
+    st = Setup(bk, lens, 2, D, "int8", seed=12)
+    st.fill()
+    q = dev(st.g.standard_normal((sum(new), 4, D)).astype(np.float16))
+    b = st.batch(new)
+    want = bk.mq_kv_attention(q, st.cache, b)
+    assert torch.equal(want, bk.mq_kv_attention(q, st.cache, b))
+    for more, longer in ((1, 8), (3, 1), (5, 30)):
+        other = bk.KVBatch(b.cu_q, b.kv_len, b.block_table, b.max_new * more, b.max_len * longer, slots=b.slots)
+        got = bk.mq_kv_attention(q, st.cache, other)
+        # each is within its own tolerance of the same value: two roundings to fp16 and two of p
+        assert ((got - want).abs().double() <= 2 * U * want.abs().double() + 2 * U * 1.5 * 6).all()
+
+
 def test_attention_rows_with_nothing_to_see(bk):
     """Empty sequences and sequences with more new tokens than tokens: zeros, not NaN."""
     st = Setup(bk, [0, 2, 70], 2, 64, "int8", seed=1)
