@@ -58,6 +58,17 @@ __device__ __forceinline__ void stage(Tile<D>& t, const KvView& kv, const Seq& q
   const int have = min(max(before - p0, 0), kKvBlock);
   const _Float16* kx = kr.p + (int64_t)(q.q0 + p0 - before) * kr.stride + (int64_t)h * D;   // token 0's row, new or not
   const _Float16* vx = vr.p + (int64_t)(q.q0 + p0 - before) * vr.stride + (int64_t)h * D;
+  // the block's earlier tokens, turned when they came: requested first, laid last
+  constexpr int TP = kKvBlock * (D / 8) / 256;
+  half8_t kt[TP], vt[TP];
+  if (have > 0) {
+    const int64_t base = ((int64_t)max(q.slot, 0) * kv.hk + h) * kKvBlock * D;
+#pragma unroll
+    for (int i = 0; i < TP; ++i) {   // the whole tail: what is not the sequence's is not looked at
+      kt[i] = *reinterpret_cast<const half8_t*>(kv.kt + base + 8 * (tid + 256 * i));
+      vt[i] = *reinterpret_cast<const half8_t*>(kv.vt + base + 8 * (tid + 256 * i));
+    }
+  }
   if (VEC) {
     // values: the same piece of two tokens, so that a pair is written whole (half of it may be an older token's, below)
     constexpr int VP = kKvBlock / 2 * (D / 8) / 256;
@@ -113,19 +124,14 @@ __device__ __forceinline__ void stage(Tile<D>& t, const KvView& kv, const Seq& q
       put_value(t, tok, d, vx[(int64_t)tok * vr.stride + d]);
     }
   }
-  if (have > 0) {   // the block's earlier tokens, turned when they came
-    const int64_t base = ((int64_t)max(q.slot, 0) * kv.hk + h) * kKvBlock * D;
-    for (int e = tid; e < have * (D / 8); e += 256) {
-      const int tok = e / (D / 8), d = 8 * (e % (D / 8));
-      *reinterpret_cast<half8_t*>(&t.k[tok][d]) = *reinterpret_cast<const half8_t*>(kv.kt + base + (int64_t)tok * D + d);
-    }
-    for (int e = tid; e < D * 8; e += 256) {
-      const int d = e >> 3, tok = 8 * (e & 7);
-      if (tok >= have) continue;
-      const half8_t x = *reinterpret_cast<const half8_t*>(kv.vt + base + (int64_t)d * kKvBlock + tok);
+  if (have > 0) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (tok + i < have) put_value(t, tok + i, d, x[i]);
+    for (int i = 0; i < TP; ++i) {
+      const int e = tid + 256 * i, tok = e / (D / 8), d = e >> 3, vtok = 8 * (e & 7);
+      if (tok < have) *reinterpret_cast<half8_t*>(&t.k[tok][8 * (e % (D / 8))]) = kt[i];
+#pragma unroll
+      for (int x = 0; x < 8; ++x)
+        if (vtok + x < have) put_value(t, vtok + x, d, vt[i][x]);
     }
   }
 }
