@@ -69,6 +69,12 @@ __device__ __forceinline__ _Float16 turned(const _Float16* x, int d, const RopeV
   return (_Float16)(d == a ? y.x : y.y);
 }
 
+// Eight fp16 values from or to any element of a tensor: one 16-byte access, which memory takes at any address.
+typedef _Float16 half8_any_t __attribute__((ext_vector_type(8), aligned(2)));
+typedef float float4_any_t __attribute__((ext_vector_type(4), aligned(4)));
+__device__ __forceinline__ half8_t load8(const _Float16* p) { return *reinterpret_cast<const half8_any_t*>(p); }
+__device__ __forceinline__ void store8(_Float16* p, const half8_t& v) { *reinterpret_cast<half8_any_t*>(p) = v; }
+
 // Eight pairs (half layout: a the first elements, b the second ones) or four (interleaved: a) turned by the cosines and
 // sines of NP pairs.
 template <bool INTER, int NP>
@@ -86,15 +92,14 @@ __device__ __forceinline__ void turn_piece(half8_t& a, half8_t& b, const float2*
   }
 }
 
-// (cos, sin) of NP pairs from pair i0 on at position p, the sines times dir; NaN outside the table. NP and i0 are even,
-// so the table is read in 16-byte pieces.
+// (cos, sin) of NP pairs from pair i0 on at position p, the sines times dir; NaN outside the table.
 template <int NP>
 __device__ __forceinline__ void load_cos_sin(const RopeView& r, int64_t p, int i0, float dir, float2* cs) {
   if ((uint64_t)p < (uint64_t)r.positions) {
-    const float4* row = reinterpret_cast<const float4*>(r.table + p * (r.rot >> 1) + i0);
+    const float4_any_t* row = reinterpret_cast<const float4_any_t*>(r.table + p * (r.rot >> 1) + i0);
 #pragma unroll
     for (int i = 0; i < NP / 2; ++i) {
-      const float4 f = row[i];
+      const float4_t f = row[i];
       cs[2 * i] = make_float2(f.x, f.y * dir);
       cs[2 * i + 1] = make_float2(f.z, f.w * dir);
     }
@@ -104,13 +109,8 @@ __device__ __forceinline__ void load_cos_sin(const RopeView& r, int64_t p, int i
   }
 }
 
-// Whether a rotation's pairs fall into 16-byte pieces, and a tensor's rows too.
-inline bool piecewise(const RopeView& r) {
-  return r.rot % (r.interleaved ? 8 : 16) == 0 && (reinterpret_cast<uintptr_t>(r.table) & 15u) == 0;
-}
-inline bool wide_rows(const void* p, int64_t stride) {
-  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && stride % 8 == 0;
-}
+// Whether a rotation's pairs fall into pieces of 8 elements.
+inline bool piecewise(const RopeView& r) { return r.rot % (r.interleaved ? 8 : 16) == 0; }
 
 __device__ __forceinline__ bool finite_h(_Float16 v) {
   return (__builtin_bit_cast(uint16_t, v) & 0x7C00u) != 0x7C00u;

@@ -49,8 +49,8 @@ __device__ __forceinline__ void put_value(Tile<D>& t, int tok, int d, _Float16 x
   reinterpret_cast<_Float16*>(&t.v[d][pair_place(d, tok >> 1)])[tok & 1] = x;
 }
 
-// The 64 keys and values of the block at p0 of sequence q into LDS, the new keys turned. VEC: new rows are read in
-// 16-byte pieces, a rotation works on whole pieces.
+// The 64 keys and values of the block at p0 of sequence q into LDS, the new keys turned. VEC: the rotation, if any,
+// works on whole pieces of 8 elements.
 template <int D, bool VEC>
 __device__ __forceinline__ void stage(Tile<D>& t, const KvView& kv, const Seq& q, int h, int p0, RowsIn kr, RowsIn vr,
                                       const RopeView& rope) {
@@ -77,13 +77,13 @@ __device__ __forceinline__ void stage(Tile<D>& t, const KvView& kv, const Seq& q
     for (int i = 0; i < VP; ++i) {
       const int e = tid + 256 * i, pair = e / (D / 8), d = 8 * (e % (D / 8));
       va[i] = vb[i] = (half8_t)(_Float16)0.0f;
-      if (2 * pair >= have) va[i] = *reinterpret_cast<const half8_t*>(vx + (int64_t)(2 * pair) * vr.stride + d);
-      if (2 * pair + 1 >= have) vb[i] = *reinterpret_cast<const half8_t*>(vx + (int64_t)(2 * pair + 1) * vr.stride + d);
+      if (2 * pair >= have) va[i] = load8(vx + (int64_t)(2 * pair) * vr.stride + d);
+      if (2 * pair + 1 >= have) vb[i] = load8(vx + (int64_t)(2 * pair + 1) * vr.stride + d);
     }
     const int half = rope.rot >> 1, turns = !rope.table ? 0 : rope.interleaved ? rope.rot >> 3 : rope.rot >> 4;
     const int rest = rope.table ? (D - rope.rot) >> 3 : D / 8, units = turns + rest;
     const auto key_piece = [&](int tok, int d) {
-      return *reinterpret_cast<const half8_t*>(kx + (int64_t)tok * kr.stride + d);
+      return load8(kx + (int64_t)tok * kr.stride + d);
     };
     for (int e = tid; e < kKvBlock * units; e += 256) {
       const int tok = e / units, u = e % units;
@@ -257,8 +257,8 @@ __device__ __forceinline__ void turn_queries(const Seq& q, int t0, int t1, int h
 #pragma unroll
       for (int h = 0; h < HP; ++h) {
         if (h0 + h < hq) {
-          a[h] = *reinterpret_cast<const half8_t*>(x + h * D + d);
-          if (two) b[h] = *reinterpret_cast<const half8_t*>(x + h * D + d + half);
+          a[h] = load8(x + h * D + d);
+          if (two) b[h] = load8(x + h * D + d + half);
         }
       }
       float2 cs[8];
@@ -271,11 +271,11 @@ __device__ __forceinline__ void turn_queries(const Seq& q, int t0, int t1, int h
         if (h0 + h < hq) {
           if (two) {
             turn_piece<false, 8>(a[h], b[h], cs);
-            *reinterpret_cast<half8_t*>(y + h * D + d + half) = b[h];
+            store8(y + h * D + d + half, b[h]);
           } else if (!pass) {
             turn_piece<true, 4>(a[h], a[h], cs);
           }
-          *reinterpret_cast<half8_t*>(y + h * D + d) = a[h];
+          store8(y + h * D + d, a[h]);
         }
       }
     }
@@ -374,8 +374,7 @@ template <int D, int FMT>
 hipError_t go(const KvView& kv, const BatchView& b, RowsIn q, int hq, RowsIn k, RowsIn v, const RopeView& rope,
               RowsOut qo, int touched, int kv_groups, int q_tokens, int q_groups, int groups, hipStream_t s) {
   const dim3 g((unsigned)groups), t(256);
-  const bool vec = wide_rows(k.p, k.stride) && wide_rows(v.p, v.stride) && (!rope.table || piecewise(rope)) &&
-                   (q_groups == 0 || (wide_rows(q.p, q.stride) && wide_rows(qo.p, qo.stride)));
+  const bool vec = !rope.table || piecewise(rope);
   if (vec)
     k_append<D, FMT, true><<<g, t, 0, s>>>(kv, b, q, hq, k, v, rope, qo, touched, kv_groups, q_tokens, q_groups);
   else

@@ -26,55 +26,56 @@ __device__ __forceinline__ float sum_group(float v, float* lds) {
   return t;
 }
 
-// 8 elements from p (or those of them below `left`, one by one, where the
-// rows do not allow 16-byte accesses or end inside the piece).
-template <bool VEC, typename T>
-__device__ __forceinline__ void load8(const T* p, int left, float* v) {
-  if (VEC) {
-    if (left > 0) {
-      if (sizeof(T) == 2) {
-        const half8_t h = *reinterpret_cast<const half8_t*>(p);
+// 8 elements from p, or the first `left` of them one by one where the row ends; rows may start anywhere.
+__device__ __forceinline__ void take8(const _Float16* p, int left, float* v) {
+  if (left >= 8) {
+    const half8_t h = load8(p);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = (float)h[i];
-      } else {
-        const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = 0.0f;
-    }
+    for (int i = 0; i < 8; ++i) v[i] = (float)h[i];
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = i < left ? (float)p[i] : 0.0f;
   }
 }
-
-template <bool VEC, typename T>
-__device__ __forceinline__ void store8(T* p, int left, const float* v) {
-  if (VEC) {
-    if (left > 0) {
-      if (sizeof(T) == 2) {
-        half8_t h;
+__device__ __forceinline__ void take8(const float* p, int left, float* v) {
+  if (left >= 8) {
+    const float4_t a = reinterpret_cast<const float4_any_t*>(p)[0], b = reinterpret_cast<const float4_any_t*>(p + 4)[0];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) h[i] = (_Float16)v[i];
-        *reinterpret_cast<half8_t*>(p) = h;
-      } else {
-        reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-        reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-      }
+    for (int i = 0; i < 4; ++i) {
+      v[i] = a[i];
+      v[i + 4] = b[i];
     }
   } else {
 #pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i < left ? p[i] : 0.0f;
+  }
+}
+__device__ __forceinline__ void put8(_Float16* p, int left, const float* v) {
+  if (left >= 8) {
+    half8_t h;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = (_Float16)v[i];
+    store8(p, h);
+  } else {
+#pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (i < left) p[i] = (T)v[i];
+      if (i < left) p[i] = (_Float16)v[i];
+  }
+}
+__device__ __forceinline__ void put8(float* p, int left, const float* v) {
+  if (left >= 8) {
+    reinterpret_cast<float4_any_t*>(p)[0] = (float4_t){v[0], v[1], v[2], v[3]};
+    reinterpret_cast<float4_any_t*>(p + 4)[0] = (float4_t){v[4], v[5], v[6], v[7]};
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < left) p[i] = v[i];
   }
 }
 
-// CH pieces of 8 elements a thread. Multiply-adds are written out, so that
-// both forms of access give the same bits.
-template <typename R, bool VEC, int THREADS, int CH>
+// CH pieces of 8 elements a thread. Multiply-adds are written out, so that all
+// instances give the same bits.
+template <typename R, int THREADS, int CH>
 __global__ __launch_bounds__(THREADS) void k_norm(mq_norm_args a) {
   __shared__ float lds[2][THREADS / 64];
   const int64_t row = blockIdx.x;
@@ -86,8 +87,8 @@ __global__ __launch_bounds__(THREADS) void k_norm(mq_norm_args a) {
 #pragma unroll
   for (int c = 0; c < CH; ++c) {
     const int d = 8 * (c * THREADS + tid);
-    if (y) load8<VEC>(y + row * a.y_stride + d, width - d, x[c]);
-    load8<VEC>(r + d, width - d, v[c]);
+    if (y) take8(y + row * a.y_stride + d, width - d, x[c]);
+    take8(r + d, width - d, v[c]);
   }
   if (y) {
     float scale = a.beta;
@@ -105,7 +106,7 @@ __global__ __launch_bounds__(THREADS) void k_norm(mq_norm_args a) {
       const int d = 8 * (c * THREADS + tid), left = width - d;
       float w[8];
       if (a.w_post) {
-        load8<VEC>(static_cast<const _Float16*>(a.w_post) + d, left, w);
+        take8(static_cast<const _Float16*>(a.w_post) + d, left, w);
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[c][i] = x[c][i] * scale * (w[i] + a.weight_offset) * a.beta;
       } else {
@@ -113,14 +114,14 @@ __global__ __launch_bounds__(THREADS) void k_norm(mq_norm_args a) {
         for (int i = 0; i < 8; ++i) x[c][i] *= scale;
       }
       if (a.gate) {
-        load8<VEC>(static_cast<const _Float16*>(a.gate) + row * a.gate_stride + d, left, w);
+        take8(static_cast<const _Float16*>(a.gate) + row * a.gate_stride + d, left, w);
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[c][i] *= w[i];
       }
       // the residual as it is stored: the next norm is taken from what a later reader finds
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[c][i] = (float)(R)fp32(fmaf(a.alpha, v[c][i], x[c][i]));
-      store8<VEC>(static_cast<R*>(a.r_out) + row * a.r_out_stride + d, left, v[c]);
+      put8(static_cast<R*>(a.r_out) + row * a.r_out_stride + d, left, v[c]);
     }
   }
   if (!a.w_pre) return;
@@ -135,47 +136,38 @@ __global__ __launch_bounds__(THREADS) void k_norm(mq_norm_args a) {
   for (int c = 0; c < CH; ++c) {
     const int d = 8 * (c * THREADS + tid), left = width - d;
     float w[8];
-    load8<VEC>(static_cast<const _Float16*>(a.w_pre) + d, left, w);
+    take8(static_cast<const _Float16*>(a.w_pre) + d, left, w);
 #pragma unroll
     for (int i = 0; i < 8; ++i) w[i] = fp32(v[c][i] * scale * (w[i] + a.weight_offset));
-    store8<VEC>(static_cast<_Float16*>(a.h_out) + row * a.h_stride + d, left, w);
+    put8(static_cast<_Float16*>(a.h_out) + row * a.h_stride + d, left, w);
   }
 }
 
-template <typename R, bool VEC>
+template <typename R>
 void dispatch(const mq_norm_args& a, hipStream_t s) {
   const dim3 g((unsigned)a.tokens);
   if (a.width <= 2048)
-    k_norm<R, VEC, 256, 1><<<g, dim3(256), 0, s>>>(a);
+    k_norm<R, 256, 1><<<g, dim3(256), 0, s>>>(a);
   else if (a.width <= 4096)
-    k_norm<R, VEC, 512, 1><<<g, dim3(512), 0, s>>>(a);
+    k_norm<R, 512, 1><<<g, dim3(512), 0, s>>>(a);
   else if (a.width <= 8192)
-    k_norm<R, VEC, 1024, 1><<<g, dim3(1024), 0, s>>>(a);
+    k_norm<R, 1024, 1><<<g, dim3(1024), 0, s>>>(a);
   else if (a.width <= 16384)
-    k_norm<R, VEC, 1024, 2><<<g, dim3(1024), 0, s>>>(a);
+    k_norm<R, 1024, 2><<<g, dim3(1024), 0, s>>>(a);
   else if (a.width <= 32768)
-    k_norm<R, VEC, 1024, 4><<<g, dim3(1024), 0, s>>>(a);
+    k_norm<R, 1024, 4><<<g, dim3(1024), 0, s>>>(a);
   else
-    k_norm<R, VEC, 1024, 8><<<g, dim3(1024), 0, s>>>(a);
+    k_norm<R, 1024, 8><<<g, dim3(1024), 0, s>>>(a);
 }
 
 }  // namespace
 
 hipError_t launch_norm_residual(const mq_norm_args& a, hipStream_t s) {
   if (a.tokens == 0) return hipSuccess;
-  // 16-byte accesses where every row of every array allows them
-  const auto wide = [&](const void* p, int64_t stride, int size) {
-    return !p || ((reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (stride * size) % 16 == 0);
-  };
-  const int rs = a.residual_fp32 ? 4 : 2;
-  const bool vec = a.width % 8 == 0 && wide(a.y, a.y_stride, 2) && wide(a.r, a.r_stride, rs) &&
-                   wide(a.gate, a.gate_stride, 2) && wide(a.w_post, 0, 2) && wide(a.w_pre, 0, 2) &&
-                   wide(a.y ? a.r_out : nullptr, a.r_out_stride, rs) && wide(a.w_pre ? a.h_out : nullptr, a.h_stride, 2);
-  if (a.residual_fp32) {
-    if (vec) dispatch<float, true>(a, s); else dispatch<float, false>(a, s);
-  } else {
-    if (vec) dispatch<_Float16, true>(a, s); else dispatch<_Float16, false>(a, s);
-  }
+  if (a.residual_fp32)
+    dispatch<float>(a, s);
+  else
+    dispatch<_Float16>(a, s);
   return hipGetLastError();
 }
 

@@ -87,7 +87,7 @@ typedef struct {
  *                gradient; where the scaling has m != 1, m multiplies again)
  *   Y_dev_fp16   as X with its own strides; Y may be X with X's strides
  *   tokens >= 0 (0 enqueues nothing), heads >= 1, head_dim >= 2; pointers
- *   2-byte aligned (16-byte loads are used where pointers and strides allow)
+ *   2-byte aligned
  *
  * Products and sums are rounded one by one in fp32, the result once to fp16.
  * Errors: MQ_ERR_INVALID_ARG, MQ_ERR_UNSUPPORTED (tokens or heads * head_dim
@@ -162,8 +162,7 @@ typedef struct {
  * cache is written. Appending the same token again at the same position
  * gives the same cache while its block is open. Tokens with a negative
  * position, of a block past table_width, or whose block or slot is out of
- * range are dropped. 16-byte aligned rows (pointers and strides) are read
- * with wide loads. Errors: MQ_ERR_INVALID_ARG, MQ_ERR_UNSUPPORTED (head_dim
+ * range are dropped. Errors: MQ_ERR_INVALID_ARG, MQ_ERR_UNSUPPORTED (head_dim
  * not 64 or 128, more than 2^31 - 1 tokens or workgroups), MQ_ERR_DEVICE.
  */
 mq_status mq_kv_append(const mq_kv_cache* cache, const mq_kv_batch* batch, const void* q_dev_fp16, int32_t q_heads,
