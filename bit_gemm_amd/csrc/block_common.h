@@ -15,14 +15,21 @@ struct Seq {
   int slot;   // its tail slot, -1 where the table names none that exists
 };
 
+// What no thread of the kernel writes: the load may be a scalar one, where the address is uniform, also in a loop that
+// writes elsewhere.
+template <typename T>
+__device__ __forceinline__ T unwritten(const T* p) {
+  return *(const __attribute__((address_space(4))) T*)p;
+}
+
 __device__ __forceinline__ Seq seq_of(const BatchView& b, const KvView& kv, int s) {
   Seq q;
-  const int c0 = b.cu[s], c1 = b.cu[s + 1];
+  const int c0 = unwritten(b.cu + s), c1 = unwritten(b.cu + s + 1);
   q.q0 = min(max(c0, 0), b.tokens);
   q.n = min(max(c1, q.q0), b.tokens) - q.q0;
-  q.len = max(b.len[s], 0);
+  q.len = max(unwritten(b.len + s), 0);
   q.cap = (int)min((int64_t)q.len, (int64_t)b.width * kKvBlock);
-  const int slot = b.slot ? b.slot[s] : s;
+  const int slot = b.slot ? unwritten(b.slot + s) : s;
   q.slot = (unsigned)slot < (unsigned)kv.slots ? slot : -1;
   return q;
 }

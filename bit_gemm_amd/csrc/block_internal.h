@@ -62,9 +62,10 @@ constexpr int attn_rows(int dim) { return dim == 64 ? 128 : 256; }
 // How the attention of a batch is run: a rule on sizes alone (kv_attn.hip).
 struct AttnPlan {
   int nt;             // blocks of 16 query rows a workgroup holds; 0: the kernel for many rows, attn_rows of them
-  int row_tiles;      // workgroups along the rows of the longest sequence
-  int chunk;          // cache blocks of one workgroup
-  int splits;         // workgroups along the cache of the longest sequence; 1: no workspace
+  int row_tiles;      // row tiles of the sequence with the most rows
+  bool slices;        // many rows: a workgroup takes a slice of all the work, whatever row tiles that is of
+  int chunk;          // else: cache blocks of one workgroup
+  int splits;         // and workgroups along the cache of the longest sequence; 1: no workspace
   int64_t groups;     // workgroups in all
   size_t bytes;       // workspace
 };

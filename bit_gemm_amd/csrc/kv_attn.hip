@@ -336,6 +336,7 @@ hipError_t go(const AttnArgs& A, const AttnPlan& p, hipStream_t s) {
   hipError_t e = hipSuccess;
   if (p.nt == 0) {
     e = launch_attn_rows(A, D, FMT, p, s);
+    if (p.slices) return e;
   } else {
     if (p.nt == 1) k_attn_split<D, FMT, 1><<<g, ts, 0, s>>>(A);
     if (p.nt == 2) k_attn_split<D, FMT, 2><<<g, ts, 0, s>>>(A);
@@ -372,21 +373,27 @@ AttnPlan plan_attention(int hk, int hq, int dim, int64_t seqs, int64_t tokens, i
     one = seqs * p.row_tiles * hk;
     splits = one > 0 ? std::min(up(256, one), up(blocks, 2 * kWaves)) : 1;
   } else {
-    // Workgroups before any split, as far as the host can tell: the tokens give the row tiles that there are, where
-    // sequences differ in length. While they leave half of the places on the GPU idle the cache is split to fill them
-    // once, in parts of 4 blocks at least; else, to even out, to fill them about twice, in parts of 16.
+    // Row tiles that there are, as far as the host can tell: the tokens give their number where sequences differ in
+    // length. While they leave half of the places on the GPU idle the cache is split to fill them once, in parts of 4
+    // blocks at least. While they do not fill the places twice they run in slices of one size (kv_attn_rows.hip): 3
+    // prompts of 500 to 2000 on up to 4000 188 us, in splits 204 to 312 for one to four of them; few tiles the other way: 16
+    // tokens on 3000 29 us in slices, 13 in splits. Else one workgroup a tile.
     const int64_t tile = attn_rows(dim), places = 256 * 256 / tile;
     p.row_tiles = (int)up(rows, tile);
     one = seqs * p.row_tiles * hk;
     const int64_t there = std::min(seqs * p.row_tiles, tokens * (hq / hk) / tile + seqs) * hk;
-    splits = one <= 0                                  ? 1
-             : 2 * there <= places && blocks >= 16 ? std::min(places / there, up(blocks, 4))
-                                                       : std::min(up(2 * places, there), up(blocks, 16));
+    p.slices = one > 0 && blocks >= 16 && 2 * there > places && there < 2 * places;
+    splits = one > 0 && blocks >= 16 && 2 * there <= places ? std::min(places / there, up(blocks, 4)) : 1;
   }
   if (splits > 256) splits = 256;
   p.chunk = (int)up(blocks, splits);
   p.splits = (int)up(blocks, p.chunk);
   p.groups = one * p.splits;
+  if (p.slices) {
+    p.groups = 256 * 256 / attn_rows(dim);
+    p.bytes = (size_t)p.groups * (2 * attn_rows(dim) * ((size_t)dim * 4 + 8) + sizeof(SlicePart));
+    return p;
+  }
   p.bytes = p.splits == 1 ? 0 : (size_t)(tokens * hq) * p.splits * ((size_t)dim * 4 + 8);
   return p;
 }
@@ -407,7 +414,9 @@ hipError_t launch_kv_attention(const KvView& kv, int dim, int format, const Batc
   A.chunk = plan.chunk;
   A.splits = plan.splits;
   A.ws_o = static_cast<float*>(ws);
-  A.ws_ml = reinterpret_cast<float2*>(A.ws_o + (size_t)b.tokens * hq * plan.splits * dim);
+  const size_t parts = plan.slices ? (size_t)plan.groups * 2 * attn_rows(dim) : (size_t)b.tokens * hq * plan.splits;
+  A.ws_ml = reinterpret_cast<float2*>(A.ws_o + parts * dim);
+  A.ws_parts = reinterpret_cast<SlicePart*>(A.ws_ml + parts);
   if (dim == 64)
     return format == MQ_KV_INT8 ? go<64, MQ_KV_INT8>(A, plan, s) : go<64, MQ_KV_E4M3>(A, plan, s);
   return format == MQ_KV_INT8 ? go<128, MQ_KV_INT8>(A, plan, s) : go<128, MQ_KV_E4M3>(A, plan, s);

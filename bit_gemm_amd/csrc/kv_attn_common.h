@@ -29,6 +29,13 @@ __device__ __forceinline__ half8_t widen8(uint32_t a, uint32_t b) {
   return __builtin_bit_cast(half8_t, r);
 }
 
+// What a workgroup of k_attn_slices says of its slice, for the join: flags, the tile that begins in it and goes on, the
+// slice's number and how many there are.
+enum { kPartOf = 1, kPartEnds = 2, kPartBegins = 4 };   // it goes on with a tile; that tile ends in it; one begins and goes on
+struct SlicePart {
+  int flags, s, h, rt, w, slices;
+};
+
 struct AttnArgs {
   KvView kv;
   BatchView b;
@@ -37,8 +44,9 @@ struct AttnArgs {
   int hq, group, causal;
   float scale2;     // scale log2(e): scores are in units of the 2-based exponent
   int row_tiles, chunk, splits;
-  float* ws_o;      // [tokens][q heads][splits][D] unnormalised sums
-  float2* ws_ml;    // [tokens][q heads][splits] (m, l); l = 0: nothing seen
+  float* ws_o;      // unnormalised sums, [tokens][q heads][splits][D]; of slices [workgroups][2][rows][D]
+  float2* ws_ml;    // likewise (m, l); l = 0: nothing seen
+  SlicePart* ws_parts;   // [workgroups]
 };
 
 // The kernel for many query rows (kv_attn_rows.hip).
