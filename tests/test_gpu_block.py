@@ -320,13 +320,14 @@ def test_append_drops_what_has_no_place(bk):
 
 
 # ---------------------------------------------------------------- attention
-def check_attention(st, q, new, causal, scale=None, what="", rows=None, lens=None):
+def check_attention(st, q, new, causal, scale=None, what="", rows=None, lens=None, batch=None):
     D, hk = st.D, st.hk
     lens = st.lens if lens is None else lens
     hq = q.shape[1]
     scale = D ** -0.5 if scale is None else scale
     qn = q.cpu().numpy().astype(np.float64)
-    got = st.bk.mq_kv_attention(q, st.cache, st.batch(new, lens), causal=causal, scale=scale).cpu().numpy()
+    batch = batch or st.batch(new, lens)
+    got = st.bk.mq_kv_attention(q, st.cache, batch, causal=causal, scale=scale).cpu().numpy()
     at = 0
     for s, n in enumerate(new):
         L = lens[s]
@@ -388,6 +389,88 @@ def test_attention_of_long_pieces(bk, new, lens, hq, hk, D, causal, fmt):
     q = dev((st.g.standard_normal((sum(new), hq, D)) * 1.5).astype(np.float16))
     rows = sorted({0, 1, 31, 32, 62, 63, 64, 65, 127, 128, 129, 255, 256, 299, 300, 399, 511, 512, 640, 698, 699, 999})
     check_attention(st, q, new, causal, rows=rows)
+
+
+def ragged(seed, seqs, hi, longest, empty=0.2):
+    """New tokens and lengths of a ragged batch: sequences without new tokens, without a past, longer than 15 blocks."""
+    g = np.random.default_rng(seed)
+    new = [0 if g.random() < empty else int(g.integers(1, hi + 1)) for _ in range(seqs)]
+    new[seqs // 2] = hi
+    lens = [n + (0 if g.random() < 0.3 else int(g.integers(0, longest - n))) for n in new]
+    lens[-1] = longest
+    return new, lens
+
+
+SLICES = [  # batch, query heads, kv heads, dim, causal: many row tiles, but not enough to fill the GPU twice
+    (ragged(1, 20, 150, 1100), 16, 16, 64, True),
+    (ragged(2, 20, 150, 1100), 16, 16, 64, False),
+    (ragged(3, 9, 160, 1300), 32, 16, 128, True),
+    (ragged(4, 9, 160, 1300), 16, 16, 128, False),
+    (ragged(5, 130, 90, 1000, 0.5), 3, 3, 64, True),    # more sequences than a wave has lanes
+    (([0, 0, 700, 0], [0, 100, 4000, 64]), 48, 24, 64, True),
+    (([300], [2000]), 99, 99, 64, True),
+    (([520, 260, 1], [520, 2050, 1]), 25, 25, 128, True),
+]
+
+
+def in_slices(bk, st, b, tokens, hq):
+    """Whether the call lays its work out in slices: the size of its workspace is that of no split."""
+    rows = 128 if st.D == 64 else 256
+    return bk.kv_attention_workspace(st.cache, b, tokens, hq) == 65536 // rows * (2 * rows * (4 * st.D + 8) + 24)
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("batch,hq,hk,D,causal", SLICES)
+def test_attention_in_slices(bk, batch, hq, hk, D, causal, fmt):
+    import torch
+    new, lens = batch
+    print("slices", new, lens, hq, hk, D, causal, fmt, flush=True)
+    st = Setup(bk, lens, hk, D, fmt, seed=sum(new) + D)
+    st.fill()
+    q = dev((st.g.standard_normal((sum(new), hq, D)) * 1.5).astype(np.float16))
+    b = st.batch(new)
+    assert in_slices(bk, st, b, len(q), hq)
+    got = check_attention(st, q, new, causal, rows=[0, 1, 31, 63, 64, 89, 127, 128, 149, 159, 259, 299, 519, 699])
+    # what was in the workspace before does not matter, and the same call gives the same bits
+    ws = torch.full((bk.kv_attention_workspace(st.cache, b, len(q), hq),), 255, dtype=torch.uint8, device="cuda")
+    again = bk.mq_kv_attention(q, st.cache, b, causal=causal, workspace=ws).cpu().numpy()
+    assert np.array_equal(got.view(np.int16), again.view(np.int16))
+
+
+def test_slices_of_rows_with_nothing_to_see(bk):
+    """Sequences that are empty, or have more new tokens than tokens, among others: zeros where nothing is seen."""
+    new, lens = [130, 40, 129, 0, 200, 5], [0, 20, 1000, 7, 100, 5]
+    st = Setup(bk, lens, 24, 64, "int8", seed=3)
+    st.fill()
+    q = dev(st.g.standard_normal((sum(new), 48, 64)).astype(np.float16))
+    assert in_slices(bk, st, st.batch(new), len(q), 48)
+    got = check_attention(st, q, new, True, rows=[0, 19, 20, 39, 99, 100, 128, 129, 199])
+    assert not got[:130].any() and not got[130:150].any() and got[150:170].any(axis=-1).all()
+
+
+def test_slices_in_a_graph(bk):
+    """A captured call follows the lengths and the new tokens that it finds."""
+    import torch
+    new, lens, hq = [120, 60, 200, 20], [900, 1200, 500, 1030], 64
+    st = Setup(bk, lens, 32, 64, "e4m3", seed=8)
+    st.fill()
+    q = dev(st.g.standard_normal((sum(new), hq, 64)).astype(np.float16))
+    b = st.batch(new)
+    assert in_slices(bk, st, b, len(q), hq)
+    ws = torch.empty(bk.kv_attention_workspace(st.cache, b, len(q), hq), dtype=torch.uint8, device="cuda")
+    bk.mq_kv_attention(q, st.cache, b, workspace=ws)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o = bk.mq_kv_attention(q, st.cache, b, workspace=ws)
+    for n, L in ((new, lens), ([0, 200, 0, 200], [0, 1200, 64, 1030]), ([100, 100, 100, 100], [128, 640, 128, 960]),
+                 ([1, 199, 199, 1], [64, 256, 448, 1030]), (new, lens)):
+        b.cu_q.copy_(torch.tensor([0] + list(np.cumsum(n)), dtype=torch.int32))
+        b.kv_len.copy_(torch.tensor(L, dtype=torch.int32))
+        graph.replay()
+        torch.cuda.synchronize()
+        eager = bk.mq_kv_attention(q, st.cache, b)
+        assert torch.equal(o.view(torch.int16), eager.view(torch.int16)), (n, L)
+        check_attention(st, q, n, True, rows=[0, 63, 99, 128, 198, 199], lens=L, batch=b)
 
 
 @pytest.mark.parametrize("new,hq", [([2], 4), ([90], 4)])
