@@ -14,6 +14,8 @@
 //                tail, after its reads, since they may take the same places.
 // Bound by HBM for prompts (rows read once, codes written once), by the chain
 // of dependent loads (offsets, position, rotation, store) for single tokens.
+// 4 prompts of 700 to 4096 tokens, 32 query and 8 kv heads of 128 (185 MB): 37 us
+// where a large copy would take 36; one token of 16 sequences: 6.6 us.
 #include <type_traits>
 
 #include "block_common.h"
