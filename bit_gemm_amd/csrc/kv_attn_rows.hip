@@ -585,10 +585,7 @@ __global__ __launch_bounds__(256) void k_attn_join_slices(AttnArgs A) {
   const int i = (int)blockIdx.x;
   const SlicePart mark = A.ws_parts[i];
   if (!(mark.flags & kPartBegins)) return;
-  const Seq q = seq_of(A.b, A.kv, mark.s);
-  const int x = threadIdx.x % X, r = (int)blockIdx.y * R + threadIdx.x / X;
-  const int64_t row = (int64_t)mark.rt * TR + r;
-  if (row >= (int64_t)q.n * A.group) return;
+  // how many parts: all lanes look, also those without a row
   const int per = (mark.slices + 7) / 8, lane = threadIdx.x & 63;
   int parts = 1;
   for (int w = mark.w + 1; w < mark.slices; w += 64) {
@@ -598,6 +595,10 @@ __global__ __launch_bounds__(256) void k_attn_join_slices(AttnArgs A) {
     if (any) break;
   }
   parts = min(parts, mark.slices - mark.w);
+  const Seq q = seq_of(A.b, A.kv, mark.s);
+  const int x = threadIdx.x % X, r = (int)blockIdx.y * R + threadIdx.x / X;
+  const int64_t row = (int64_t)mark.rt * TR + r;
+  if (row >= (int64_t)q.n * A.group) return;
   float top = kNoMax, total = 0.0f;
   float4_t acc = {0.0f, 0.0f, 0.0f, 0.0f};
   for (int p = 0; p < parts; p += 4) {   // four at a time

@@ -410,6 +410,8 @@ SLICES = [  # batch, query heads, kv heads, dim, causal: many row tiles, but not
     (([0, 0, 700, 0], [0, 100, 4000, 64]), 48, 24, 64, True),
     (([300], [2000]), 99, 99, 64, True),
     (([520, 260, 1], [520, 2050, 1]), 25, 25, 128, True),
+    (([0] * 40 + [65] + [0] * 30, [64] * 40 + [16000] + [0] * 30), 4, 4, 64, True),     # a tile over many slices,
+    (([0] * 40 + [257] + [0] * 30, [64] * 40 + [9000] + [0] * 30), 2, 2, 128, True),    # its last row alone in a wave
 ]
 
 
@@ -430,7 +432,7 @@ def test_attention_in_slices(bk, batch, hq, hk, D, causal, fmt):
     q = dev((st.g.standard_normal((sum(new), hq, D)) * 1.5).astype(np.float16))
     b = st.batch(new)
     assert in_slices(bk, st, b, len(q), hq)
-    got = check_attention(st, q, new, causal, rows=[0, 1, 31, 63, 64, 89, 127, 128, 149, 159, 259, 299, 519, 699])
+    got = check_attention(st, q, new, causal, rows=[0, 1, 31, 63, 64, 89, 127, 128, 149, 159, 256, 259, 299, 519, 699])
     # what was in the workspace before does not matter, and the same call gives the same bits
     ws = torch.full((bk.kv_attention_workspace(st.cache, b, len(q), hq),), 255, dtype=torch.uint8, device="cuda")
     again = bk.mq_kv_attention(q, st.cache, b, causal=causal, workspace=ws).cpu().numpy()
