@@ -98,6 +98,11 @@ def _stream(stream, t) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _like(t):
+    """A dense tensor of t's shape and type (0.6 us faster than by shape, where t is dense)."""
+    return torch.empty_like(t) if t.is_contiguous() else t.new_empty(t.shape)
+
+
 def _rows(t, name: str, heads=None, dim=None):
     """Checks an fp16 [tokens, heads, dim] GPU tensor whose heads lie dense in a
     row; gives its tokens, heads and the elements between rows (of at most one
@@ -152,7 +157,7 @@ def mq_rope(x, rope: Rope, pos, inverse: bool = False, out=None, stream=None):
     T, H, D = x.shape
     _ints(pos, "pos", (T,))
     if out is None:
-        out = x.new_empty((T, H, D))
+        out = _like(x)
     elif out.dtype is not _F16 or not out.is_cuda or out.shape != x.shape or out.stride(2) != 1:
         raise ValueError("out must be a float16 GPU tensor of x's shape with dense heads")
     xt, xh, _ = x.stride()
@@ -249,7 +254,7 @@ def mq_kv_append(q, k, v, cache: KVCache, batch: KVBatch, rope: Rope | None = No
         if q is not None:
             Tq, heads, qs = _rows(q, "q", None, D)
             if q_out is None:
-                q_out, To, qos = q.new_empty((Tq, heads, D)), Tq, heads * D
+                q_out, To, qos = _like(q), Tq, heads * D
             else:
                 To, _, qos = _rows(q_out, "q_out", heads, D)
             if Tq != T or To != T:
@@ -285,7 +290,7 @@ def mq_kv_attention(q, cache: KVCache, batch: KVBatch, causal: bool = True, scal
     D = cache.head_dim
     T, H, qs = _rows(q, "q", None, D)
     if out is None:
-        out, os_ = q.new_empty((T, H, D)), H * D
+        out, os_ = _like(q), H * D
     else:
         To, _, os_ = _rows(out, "out", H, D)
         if To != T:
@@ -346,7 +351,7 @@ def mq_norm_residual(y, r, w_pre, w_post=None, gate=None, alpha: float = 1.0, be
     if y is not None:
         yp, ys = _matrix(y, "y", _F16, shape)
         if r_out is None:
-            r_out = r.new_empty(shape)
+            r_out = _like(r)
             rp, rs = r_out.data_ptr(), W
         else:
             rp, rs = _matrix(r_out, "r_out", dt, shape)
@@ -362,7 +367,7 @@ def mq_norm_residual(y, r, w_pre, w_post=None, gate=None, alpha: float = 1.0, be
     if w_pre is not None:
         wpre = _vector(w_pre, "w_pre", W)
         if h_out is None:
-            h_out = w_pre.new_empty(shape)
+            h_out = w_pre.new_empty(shape) if y is None else _like(y)
             hp, hs = h_out.data_ptr(), W
         else:
             hp, hs = _matrix(h_out, "h_out", _F16, shape)
