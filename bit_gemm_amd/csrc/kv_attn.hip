@@ -17,8 +17,9 @@
 // values). A block's scales stay in fp32: with t = (k scale) s + log2(v scale)
 // the weights are p = 2^(t - m), so that O sums codes in units of 2^-m and no
 // block needs its own accumulator; the softmax's sum takes p / (v scale). p is
-// rounded to fp16 (relative 2^-11); its sum is not, since a block of small values
-// has small p whatever its scores. All else is fp32.
+// rounded to fp16 (relative 2^-11, down to 2^-29 of the largest: m lies 15 below
+// the largest t); its sum is not, since a block of small values has small p
+// whatever its scores. All else is fp32.
 //
 // Bound by HBM: 2 head_dim bytes for each cached token and kv head. A wave's
 // loads are never conditional and keys of its next block are requested as soon
@@ -140,7 +141,7 @@ __global__ __launch_bounds__(64 * kWaves, NT == 4 ? 1 : 2) void k_attn_split(Att
         if (masked && i >= left) p[i] = -INFINITY;
         top = fmaxf(top, p[i]);
       }
-      top = max_groups(top);
+      top = reference(max_groups(top), kMaxWeight);
       if (__any(top > m[t])) {
         const float now = fmaxf(m[t], top), shrink = __builtin_amdgcn_exp2f(m[t] - now);
         m[t] = now;

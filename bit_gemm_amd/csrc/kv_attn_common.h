@@ -6,7 +6,14 @@ namespace mq {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kNoMax = -1.0e30f;   // the reference before the first visible token: finite, below every score
+constexpr float kMaxWeight = 15.0f;  // weights 2^(t - m) reach 2^15 at most, inside fp16
+constexpr float kFar = 1 << 20;      // up to here a few powers of two can be taken from a score with little rounding
 constexpr float kZeroScale = 1.0f / (1 << 30);   // stands for the scale of values that are all zero
+
+// The reference for weights whose largest score is top: `by` below it, so that the largest weight is 2^by and one of
+// 2^-(14 + by) of it is still a normal fp16 number. Thousands of weights that small may be the whole output, where the
+// largest belong to values of about zero (by = 0: weights of 2^-24.5 of the largest were off by 41 %, smaller ones lost).
+__device__ __forceinline__ float reference(float top, float by) { return fabsf(top) < kFar ? top - by : top; }
 
 // 8 codes (two dwords) as fp16, exactly.
 template <int FMT>
