@@ -240,6 +240,17 @@ __device__ __forceinline__ void attend(const AttnArgs& A, _Float16 (&lk)[2][kKvB
       for (int d = 0; d < DT; ++d) o[d] *= shrink;
     }
   };
+  // A weight is 2^(s mul + off) with off = add - m, one operation a score. Its rounding is that of m, which is nothing for
+  // scores of usual size; where they are so large that a step of fp32 is whole powers of two, the difference of the score
+  // and m is taken first.
+  const auto far_scores = [&](Scores& sc, float top, float add, float& mul, float& off) {
+    if (__any(fabsf(top) > kFar)) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) sc.t[i >> 4][i & 15] = fmaf(sc.t[i >> 4][i & 15], mul, add) - m;
+      mul = 1.0f;
+      off = 0.0f;
+    }
+  };
 
   // Turn t: the weights of block t from its scores, the product with its values, and the scores of block t + 1; the
   // keys of block t + 2 and the values of block t + 1 are laid. X = t % 2.
@@ -251,7 +262,8 @@ __device__ __forceinline__ void attend(const AttnArgs& A, _Float16 (&lk)[2][kKvB
       if (b == open_blk) k1 = v1 = 1.0f;
       if (!(b == open_blk ? sq.slot >= 0 : (uint32_t)id_t < blocks)) k1 = __builtin_nanf("");
       v1 = v1 == 0.0f ? kZeroScale : v1;
-      const float mul = k1 * scale2, add = __builtin_amdgcn_logf(v1);
+      float mul = k1 * scale2;
+      const float add = __builtin_amdgcn_logf(v1);
       const int left = end - b * kKvBlock - 8 * f;
 #pragma unroll
       for (int i = 0; i < 32; ++i)
@@ -260,7 +272,8 @@ __device__ __forceinline__ void attend(const AttnArgs& A, _Float16 (&lk)[2][kKvB
       const bool none = top == -INFINITY;
       top = none ? kNoMax : fmaf(top, mul, add);
       follow(top);
-      const float off = add - m;
+      float off = add - m;
+      far_scores(sa, top, add, mul, off);
       float sum = 0.0f;
 #pragma unroll
       for (int i = 0; i < 32; ++i) {
@@ -303,9 +316,11 @@ __device__ __forceinline__ void attend(const AttnArgs& A, _Float16 (&lk)[2][kKvB
   float top = 0.0f;   // largest score of block t, before its scale
   const auto turn_whole = [&](Scores& now, Scores& next, int X, int t) {
     const float k1 = (uint32_t)id_t < blocks ? ks : __builtin_nanf(""), v1 = vs == 0.0f ? kZeroScale : vs;
-    const float mul = k1 * scale2, add = __builtin_amdgcn_logf(v1);
-    follow(fmaf(top, mul, add));
-    const float off = add - m;
+    float mul = k1 * scale2;
+    const float add = __builtin_amdgcn_logf(v1), peak = fmaf(top, mul, add);
+    follow(peak);
+    float off = add - m;
+    far_scores(now, peak, add, mul, off);
     next_blocks(t);
     multiply_keys(next, lk[X ^ 1]);
     float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};

@@ -50,3 +50,38 @@ def test_attention_keeps_small_weights(bk, new, lens, hq, hk, D, sink, fmt):
             assert vis > sink and np.all(o > 64 * SUB)
             d = (D + 8) * E * sa
             close(got[i, h], o, U * np.abs(o) + SUB + (U + 2 * d + (D + 8 + L / 16) * E) * pv, f"token {i} head {h}")
+
+
+# ---------------------------------------------------------- scores of any size
+def one_hot(bk, new, D, key, query, scale, L=190):
+    """Keys whose elements all equal key(token) and queries all of one value: the weight is the largest score's alone, and
+    the output its value. Each row's best key has to stand alone."""
+    st = Setup(bk, [L], 1, D, "int8", seed=D + sum(new))
+
+    def values(s, k, v):
+        k[:] = np.array([key(t) for t in range(L)], np.float16)[:, None, None]
+    st.fill(values)
+    n = new[0]
+    q = dev(np.full((n, 2, D), query, np.float16))
+    got = bk.mq_kv_attention(q, st.cache, st.batch(new), scale=scale).cpu().numpy().astype(np.float64)
+    k, v = st.ref.read(L, st.tables[0], st.slots[0], 0)
+    for i in range(n):
+        score = scale * query * k[:L - n + i + 1].sum(1)
+        best = int(np.argmax(score))
+        # far enough from the next one that nothing else has weight, in the precision of the scores too
+        assert np.sort(score)[-1] - np.sort(score)[-2] > max(200.0, 2.0 ** -20 * np.abs(score).max())
+        for h in range(2):
+            close(got[i, h], v[best], 2 * U * np.abs(v[best]) + SUB, f"token {i} head {h}")
+
+
+@pytest.mark.parametrize("new", [[1], [40], [70]])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_attention_of_scores_past_fp32_steps(bk, new, D, sign):
+    """Scores so large that a step of fp32 is many units: the weights still come from differences of scores."""
+    first, second = (52000, 60000) if sign > 0 else (1200, 300)
+
+    def key(t):
+        return {7: first, 100: second}.get(t, 300 * (10 + t * 37 % 140))
+    for L in (64 + new[0], 190, 606):
+        one_hot(bk, new, D, key, sign * 30000.0, D ** -0.5, L=L)
