@@ -5,7 +5,7 @@
 namespace mq {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kNoMax = -1.0e30f;   // the reference before the first visible token: finite, below every score
+constexpr float kNoMax = -3.4028235e38f;   // the reference before the first visible token: finite, and no score is below
 constexpr float kMaxWeight = 15.0f;  // weights 2^(t - m) reach 2^15 at most, inside fp16
 constexpr float kFar = 1 << 20;      // up to here a few powers of two can be taken from a score with little rounding
 constexpr float kZeroScale = 1.0f / (1 << 30);   // stands for the scale of values that are all zero

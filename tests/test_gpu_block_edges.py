@@ -85,3 +85,10 @@ def test_attention_of_scores_past_fp32_steps(bk, new, D, sign):
         return {7: first, 100: second}.get(t, 300 * (10 + t * 37 % 140))
     for L in (64 + new[0], 190, 606):
         one_hot(bk, new, D, key, sign * 30000.0, D ** -0.5, L=L)
+
+
+@pytest.mark.parametrize("new", [[1], [40]])
+@pytest.mark.parametrize("D", [64, 128])
+def test_attention_of_scores_far_below_zero(bk, new, D):
+    """All scores below -1e30, as a large scale makes them: the largest still takes the weight."""
+    one_hot(bk, new, D, lambda t: {7: -4, 100: -1}.get(t, -(10 + t * 37 % 100)), 1.0, 1e30)
