@@ -238,6 +238,7 @@ __global__ __launch_bounds__(64 * kWaves, NT == 4 ? 1 : 2) void k_attn_split(Att
   __shared__ float so[SIDES][16 * NT][D + 4];
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
+    if (end[t] > 0) l[t] += zero_if_finite(qf[t]);
     l[t] = sum_groups(l[t]);
     if (g == 0) {
       sm[wave][16 * t + c] = m[t];

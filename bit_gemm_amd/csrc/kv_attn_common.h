@@ -36,6 +36,19 @@ __device__ __forceinline__ half8_t widen8(uint32_t a, uint32_t b) {
   return __builtin_bit_cast(half8_t, r);
 }
 
+// 0, or NaN where one of a lane's N pieces of a query is not finite. A row's sum of weights takes it in at the end: such
+// a query has no finite score, and where all are -Inf nothing else would tell it from a row that sees nothing.
+template <int N>
+__device__ __forceinline__ float zero_if_finite(const half8_t (&q)[N]) {
+  half8_t z = q[0] * (_Float16)0.0f;
+#pragma unroll
+  for (int i = 1; i < N; ++i) z += q[i] * (_Float16)0.0f;
+  float sum = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) sum += (float)z[i];
+  return sum;
+}
+
 // What a workgroup of k_attn_slices says of its slice, for the join: flags, the tile that begins in it and goes on, the
 // slice's number and how many there are.
 enum { kPartOf = 1, kPartEnds = 2, kPartBegins = 4 };   // it goes on with a tile; that tile ends in it; one begins and goes on

@@ -367,6 +367,7 @@ __device__ __forceinline__ void attend(const AttnArgs& A, _Float16 (&lk)[2][kKvB
     }
   }
 
+  if (end > 0) l += zero_if_finite(qf);
   l = sum_halves(l);
   if (r >= rows) return;
   const AttnArgs Z = AGAIN ? arguments() : A;

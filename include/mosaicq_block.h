@@ -174,7 +174,8 @@ mq_status mq_kv_append(const mq_kv_cache* cache, const mq_kv_batch* batch, const
  * mq_kv_attention -- O = softmax(scale q K^T) V over each sequence's cache.
  * Query head h reads kv head h / (q_heads / kv_heads). With causal != 0 new
  * token i attends to the positions up to its own, kv_len - n + i, else to all
- * kv_len; a query with nothing to attend to gets zeros.
+ * kv_len; a query with nothing to attend to gets zeros, one with an Inf or NaN
+ * element that attends to anything NaN.
  *
  *   q_dev_fp16    [tokens, q_heads, head_dim], rows q_stride apart, 16-byte
  *                 aligned (pointer and stride)

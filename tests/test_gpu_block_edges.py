@@ -92,3 +92,44 @@ def test_attention_of_scores_past_fp32_steps(bk, new, D, sign):
 def test_attention_of_scores_far_below_zero(bk, new, D):
     """All scores below -1e30, as a large scale makes them: the largest still takes the weight."""
     one_hot(bk, new, D, lambda t: {7: -4, 100: -1}.get(t, -(10 + t * 37 % 100)), 1.0, 1e30)
+
+
+# --------------------------------------------------------- queries
+@pytest.mark.parametrize("new,lens,D", [([1, 1], [40, 200], 64), ([3, 1], [3000, 70], 128), ([90, 70], [100, 1500], 64),
+                                        ([80, 300], [2000, 300], 128)])
+def test_attention_of_queries_that_are_not_finite(bk, new, lens, D):
+    """A query with an infinite element has no finite score: its output is NaN whatever the signs, also where every score
+    is -Inf, and no other row's does: those stay within two roundings to fp16 and two of the weights (values of about 1) of what
+    they were (a row may move its neighbours' reference, so not every bit)."""
+    import torch
+    st = Setup(bk, lens, 2, D, "int8", seed=D + lens[0])
+
+    def values(s, k, v):
+        k[:, :, 3] = np.abs(k[:, :, 3]) + np.float16(0.5)   # one sign: all of its products with an infinity are alike
+    st.fill(values)
+    q = dev(st.g.standard_normal((sum(new), 4, D)).astype(np.float16))
+    good = bk.mq_kv_attention(q, st.cache, st.batch(new))
+    rows = [(0, 1, -np.inf), (new[0] - 1, 2, np.inf), (sum(new) - 1, 0, -np.inf), (new[0], 3, -np.inf)]
+    for t, h, x in rows:
+        q[t, h, 3] = float(x)
+    for scale in (D ** -0.5, -0.25):
+        if scale < 0:
+            good = bk.mq_kv_attention(torch.where(q.isfinite(), q, torch.ones_like(q)), st.cache, st.batch(new), scale=scale)
+        got = bk.mq_kv_attention(q, st.cache, st.batch(new), scale=scale)
+        bad = torch.zeros(q.shape[:2], dtype=torch.bool, device="cuda")
+        for t, h, _ in rows:
+            bad[t, h] = True
+        assert got[bad].isnan().all(), scale
+        assert ((got - good)[~bad].abs().double() <= 2 * U * good[~bad].abs().double() + 4 * U).all(), scale
+
+
+def test_attention_of_infinite_queries_with_nothing_to_see(bk):
+    """Zeros, as for any query that sees nothing."""
+    import torch
+    st = Setup(bk, [0, 2], 1, 64, "int8", seed=1)
+    st.fill()
+    for new in ([1, 3], [40, 50]):
+        q = torch.full((sum(new), 2, 64), float("-inf"), dtype=torch.float16, device="cuda")
+        got = bk.mq_kv_attention(q, st.cache, st.batch(new))
+        seen = new[0] + new[1] - 2
+        assert not got[:seen].any() and got[seen:].isnan().all()
