@@ -292,7 +292,8 @@ __global__ __launch_bounds__(64 * kWaves, NT == 4 ? 1 : 2) void k_attn_split(Att
 
 // Joins the splits of (token, query head) rows: Y groups of threads a row, group y takes splits y, y + Y, ...; in a
 // group thread x takes elements 4 x .. 4 x + 3. The groups' sums are added in order. One group a row where the splits
-// are few and the rows many, else all of the workgroup's.
+// are few and the rows many, else all of the workgroup's. Rows of no sequence have no partial results: what
+// is read for them is not looked at.
 template <int D, int Y>
 __global__ __launch_bounds__(256) void k_attn_join(AttnArgs A, int64_t rows) {
   constexpr int X = D / 4, R = 256 / (X * Y);   // rows of a workgroup
@@ -300,6 +301,7 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs A, int64_t rows) {
   __shared__ float part_l[256 / X];
   const int x = threadIdx.x % X, z = threadIdx.x / X, y = z % Y, n = A.splits;
   const int64_t row = min((int64_t)blockIdx.x * R + z / Y, rows - 1);
+  const int first = unwritten(A.b.cu), end = unwritten(A.b.cu + A.b.seqs);
   const float2* ml = A.ws_ml + row * n;
   const float4_t* src = reinterpret_cast<const float4_t*>(A.ws_o) + row * n * X + x;
   float top = kNoMax;
@@ -330,6 +332,7 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs A, int64_t rows) {
   }
   const float inv = total == 0.0f ? 0.0f : 1.0f / total;
   const int64_t tok = row / A.hq, hh = row % A.hq;
+  if (tok < first || tok >= end) return;
   store4(reinterpret_cast<uint16_t*>(A.out.p + tok * A.out.stride + hh * D + 4 * x), acc * inv, 4, true);
 }
 

@@ -182,7 +182,8 @@ mq_status mq_kv_append(const mq_kv_cache* cache, const mq_kv_batch* batch, const
  *   q_heads       a multiple of kv_heads, at most 64 for each kv head
  *   scale         multiplies the scores (commonly head_dim^-1/2), finite
  *   out_dev_fp16  [tokens, q_heads, head_dim], rows out_stride apart, 8-byte
- *                 aligned; written for every token of a sequence; not q
+ *                 aligned; written for every token of a sequence, rows of none
+ *                 (before cu_q[0], from cu_q[seqs] on) are left as they are; not q
  *   workspace_dev, workspace_bytes  fp32 partial results, at least
  *                 mq_kv_attention_workspace bytes (0: NULL is accepted),
  *                 16-byte aligned; calls that overlap in time need their own

@@ -133,3 +133,36 @@ def test_attention_of_infinite_queries_with_nothing_to_see(bk):
         got = bk.mq_kv_attention(q, st.cache, st.batch(new))
         seen = new[0] + new[1] - 2
         assert not got[:seen].any() and got[seen:].isnan().all()
+
+
+# ------------------------------------------------- rows of no sequence
+PADS = [  # new tokens, lengths, query heads, kv heads, dim, max_len: each way of running
+    ([1, 1], [60, 40], 8, 2, 64, 64),
+    ([1, 1], [6000, 700], 8, 2, 128, 6000),             # split, joined by whole workgroups
+    ([1, 1, 1, 1], [1500, 700, 90, 1], 64, 16, 64, 2000),  # split in few parts
+    ([100], [3000], 8, 2, 128, 3000),                   # many rows, split
+    ([90, 300], [90, 900], 4, 1, 64, 900),
+    ([120, 60, 200], [900, 1200, 500], 64, 32, 64, 1200),  # slices
+]
+
+
+@pytest.mark.parametrize("new,lens,hq,hk,D,longest", PADS)
+def test_attention_leaves_rows_of_no_sequence_alone(bk, new, lens, hq, hk, D, longest):
+    """Rows before the first sequence's and behind the last one's, as in a step padded to a captured size: not written,
+    however the work is split and whatever the workspace holds."""
+    import torch
+    st = Setup(bk, lens, hk, D, "int8", seed=sum(lens))
+    st.fill()
+    first, last = 2, 5
+    T = first + sum(new) + last
+    cu = np.concatenate([[0], np.cumsum(new)]).astype(np.int32) + first
+    b = bk.KVBatch(dev(cu), dev(np.array(lens, np.int32)), st.table, max(new), longest, slots=st.dslots)
+    q = dev(st.g.standard_normal((T, hq, D)).astype(np.float16))
+    want = bk.mq_kv_attention(q[first:T - last].contiguous(), st.cache, st.batch(new))
+    ws = torch.full((max(1, bk.kv_attention_workspace(st.cache, b, T, hq)),), 255, dtype=torch.uint8, device="cuda")
+    out = torch.full((T, hq, D), 7.0, dtype=torch.float16, device="cuda")
+    bk.mq_kv_attention(q, st.cache, b, out=out, workspace=ws)
+    assert (out[:first] == 7).all() and (out[T - last:] == 7).all()
+    # the padding may change how the work is split, so not every bit: two roundings to fp16, two of the weights
+    got = out[first:T - last]
+    assert ((got - want).abs().double() <= 2 * U * want.abs().double() + 4 * U).all()
