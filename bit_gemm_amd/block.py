@@ -160,6 +160,8 @@ def mq_rope(x, rope: Rope, pos, inverse: bool = False, out=None, stream=None):
         out = _like(x)
     elif out.dtype is not _F16 or not out.is_cuda or out.shape != x.shape or out.stride(2) != 1:
         raise ValueError("out must be a float16 GPU tensor of x's shape with dense heads")
+    if T == 0:
+        return out
     xt, xh, _ = x.stride()
     yt, yh, _ = out.stride()
     code = lib.mq_rope(x.data_ptr(), T, H, D, xt, xh, pos.data_ptr(), rope._ref, int(inverse), out.data_ptr(), yt, yh,

@@ -166,3 +166,14 @@ def test_attention_leaves_rows_of_no_sequence_alone(bk, new, lens, hq, hk, D, lo
     # the padding may change how the work is split, so not every bit: two roundings to fp16, two of the weights
     got = out[first:T - last]
     assert ((got - want).abs().double() <= 2 * U * want.abs().double() + 4 * U).all()
+
+
+def test_rope_of_no_tokens(bk):
+    import torch
+    r = bk.Rope(64, 10)
+    x, pos = torch.zeros((3, 2, 64), dtype=torch.float16, device="cuda"), torch.zeros(3, dtype=torch.int32, device="cuda")
+    assert bk.mq_rope(x[:0], r, pos[:0]).shape == (0, 2, 64)
+    out = x[:0].clone()
+    assert bk.mq_rope(torch.empty((0, 2, 64), dtype=torch.float16, device="cuda"), r, pos[:0], out=out) is out
+    with pytest.raises(ValueError):
+        bk.mq_rope(x[:0], r, pos)
