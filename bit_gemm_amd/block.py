@@ -9,7 +9,9 @@ decoder block's 4-bit linears.
     r, h = mq_norm_residual(y, r, w_pre)                    # r' = r + y, h = norm(r') w_pre
 
 Argument marshalling only: every step runs in the HIP library, on the given
-stream (the current one by default), without synchronising. Importing this
+stream (the current one by default), without synchronising. What a call makes
+(outputs, workspace) comes from that stream's memory pool; the caller orders
+the streams, and keeps what a call reads until it has run. Importing this
 module fails loudly when the library is not built -- there is no fallback path.
 """
 from __future__ import annotations
@@ -98,6 +100,31 @@ def _stream(stream, t) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _other(stream, index: int):
+    """The stream a call is given, where that is not the current one anyway; None else."""
+    if stream is None:
+        return None
+    handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if handle == _current_stream(index):
+        return None
+    if hasattr(stream, "cuda_stream"):
+        return stream
+    return torch.cuda.ExternalStream(handle, device=index) if handle else torch.cuda.default_stream(index)
+
+
+def _new(other, make, *args):
+    """The new tensor make(*args) for a call on stream `other` (None: the current one). It comes from that stream's
+    pool: the current one's may hand out memory that work queued there still uses. It goes back to that pool only when
+    the current stream is done with it too, where the caller reads it."""
+    if other is None:
+        return make(*args)
+    now = torch.cuda.current_stream(other.device)
+    with torch.cuda.stream(other):
+        t = make(*args)
+    t.record_stream(now)
+    return t
+
+
 def _like(t):
     """A dense tensor of t's shape and type (0.6 us faster than by shape, where t is dense)."""
     return torch.empty_like(t) if t.is_contiguous() else t.new_empty(t.shape)
@@ -138,8 +165,9 @@ class Rope:
             raise ValueError(f"layout is one of {list(LAYOUTS)}, scaling one of {list(SCALINGS)}")
         self.rot_dim, self.positions, self.layout = int(rot_dim), int(positions), layout
         spec = _RopeSpec(self.rot_dim, SCALINGS[scaling], theta, factor, original, turns_fast, turns_slow)
-        self.table = torch.empty((max(self.positions, 1), max(self.rot_dim // 2, 1), 2), dtype=torch.float32,
-                                 device="cuda")
+        shape = (max(self.positions, 1), max(self.rot_dim // 2, 1), 2)
+        other = None if stream is None else _other(stream, torch.cuda.current_device())
+        self.table = _new(other, lambda: torch.empty(shape, dtype=torch.float32, device="cuda"))
         _check(lib.mq_rope_table(ctypes.byref(spec), self.positions, self.table.data_ptr(),
                                  _stream(stream, self.table)), "mq_rope_table")
         self._plan = _RopePlan(self.table.data_ptr(), self.positions, self.rot_dim, LAYOUTS[layout])
@@ -157,7 +185,7 @@ def mq_rope(x, rope: Rope, pos, inverse: bool = False, out=None, stream=None):
     T, H, D = x.shape
     _ints(pos, "pos", (T,))
     if out is None:
-        out = _like(x)
+        out = _like(x) if stream is None else _new(_other(stream, x.get_device()), _like, x)
     elif out.dtype is not _F16 or not out.is_cuda or out.shape != x.shape or out.stride(2) != 1:
         raise ValueError("out must be a float16 GPU tensor of x's shape with dense heads")
     if T == 0:
@@ -256,7 +284,8 @@ def mq_kv_append(q, k, v, cache: KVCache, batch: KVBatch, rope: Rope | None = No
         if q is not None:
             Tq, heads, qs = _rows(q, "q", None, D)
             if q_out is None:
-                q_out, To, qos = _like(q), Tq, heads * D
+                q_out = _like(q) if stream is None else _new(_other(stream, q.get_device()), _like, q)
+                To, qos = Tq, heads * D
             else:
                 To, _, qos = _rows(q_out, "q_out", heads, D)
             if Tq != T or To != T:
@@ -291,8 +320,9 @@ def mq_kv_attention(q, cache: KVCache, batch: KVBatch, causal: bool = True, scal
     Enqueued on `stream` (no sync)."""
     D = cache.head_dim
     T, H, qs = _rows(q, "q", None, D)
+    other = None if stream is None else _other(stream, q.get_device())
     if out is None:
-        out, os_ = _like(q), H * D
+        out, os_ = _new(other, _like, q), H * D
     else:
         To, _, os_ = _rows(out, "out", H, D)
         if To != T:
@@ -306,9 +336,7 @@ def mq_kv_attention(q, cache: KVCache, batch: KVBatch, causal: bool = True, scal
             raise TypeError("workspace must be a contiguous uint8 tensor on the GPU")
         wp, nw = workspace.data_ptr(), workspace.numel()
     elif need:
-        ws = torch.empty(need, dtype=torch.uint8, device=q.device)
-        if stream is not None:   # its memory is not given out again before the kernels are done
-            ws.record_stream(stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream)))
+        ws = _new(other, lambda: torch.empty(need, dtype=torch.uint8, device=q.device))
         wp, nw = ws.data_ptr(), need
     code = lib.mq_kv_attention(cache._ref, batch._with(T), q.data_ptr(), H, qs, int(causal),
                                D ** -0.5 if scale is None else scale, out.data_ptr(), os_, wp, nw, _stream(stream, q))
@@ -349,11 +377,12 @@ def mq_norm_residual(y, r, w_pre, w_post=None, gate=None, alpha: float = 1.0, be
         raise ValueError("r must be [tokens, width] with dense rows")
     shape, dt = r.shape, r.dtype
     M, W = shape
+    other = None if stream is None else _other(stream, r.get_device())
     yp = gp = rp = hp = wpost = wpre = ys = gs = rs = hs = 0
     if y is not None:
         yp, ys = _matrix(y, "y", _F16, shape)
         if r_out is None:
-            r_out = _like(r)
+            r_out = _new(other, _like, r)
             rp, rs = r_out.data_ptr(), W
         else:
             rp, rs = _matrix(r_out, "r_out", dt, shape)
@@ -369,7 +398,7 @@ def mq_norm_residual(y, r, w_pre, w_post=None, gate=None, alpha: float = 1.0, be
     if w_pre is not None:
         wpre = _vector(w_pre, "w_pre", W)
         if h_out is None:
-            h_out = w_pre.new_empty(shape) if y is None else _like(y)
+            h_out = _new(other, w_pre.new_empty, shape) if y is None else _new(other, _like, y)
             hp, hs = h_out.data_ptr(), W
         else:
             hp, hs = _matrix(h_out, "h_out", _F16, shape)

@@ -177,3 +177,65 @@ def test_rope_of_no_tokens(bk):
     assert bk.mq_rope(torch.empty((0, 2, 64), dtype=torch.float16, device="cuda"), r, pos[:0], out=out) is out
     with pytest.raises(ValueError):
         bk.mq_rope(x[:0], r, pos)
+
+
+# ----------------------------------------------------------------- streams
+def freed(nbytes):
+    """Addresses of a block of this size that the current stream's pool has just got back."""
+    import torch
+    t = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+    at = t.data_ptr()
+    del t
+    return range(at, at + nbytes)
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_outputs_on_another_stream_are_not_the_current_ones_memory(bk, raw):
+    """Memory that work queued on the current stream may still use is not given to a call on another stream: its outputs
+    come from that stream's pool."""
+    import torch
+    st = Setup(bk, [300, 90], 2, 64, "int8", seed=1)
+    st.fill()
+    r = bk.Rope(64, 400)
+    x = torch.zeros((2, 4, 64), dtype=torch.float16, device="cuda")
+    y = torch.zeros((2, 512), dtype=torch.float16, device="cuda")
+    w = torch.ones(512, dtype=torch.float16, device="cuda")
+    pos = torch.zeros(2, dtype=torch.int32, device="cuda")
+    b = st.batch([1, 1])
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    s = side.cuda_stream if raw else side
+    calls = {
+        "rope": (lambda: [bk.mq_rope(x, r, pos, stream=s)], x.nbytes),
+        "append": (lambda: [bk.mq_kv_append(x, x[:, :2].contiguous(), x[:, 2:].contiguous(), st.cache, b, rope=r, stream=s)], x.nbytes),
+        "attention": (lambda: [bk.mq_kv_attention(x, st.cache, b, stream=s)], x.nbytes),
+        "norm": (lambda: list(bk.mq_norm_residual(y, y, w, stream=s)), y.nbytes),
+        "table": (lambda: [bk.Rope(64, 400, stream=s).table], 400 * 32 * 8),
+    }
+    for name, (call, nbytes) in calls.items():
+        block = freed(nbytes)
+        outs = call()
+        side.synchronize()
+        assert all(o.data_ptr() not in block for o in outs), name
+
+
+def test_attention_on_two_streams_with_work_pending(bk):
+    """Two split calls, one on the current stream behind queued work, the other on a stream of its own without a wait
+    between them: each has its own workspace and gives what it gives alone."""
+    import torch
+    st = Setup(bk, [3000, 2500], 2, 128, "int8", seed=2)
+    st.fill()
+    b = st.batch([1, 1])
+    q1, q2 = (dev(st.g.standard_normal((2, 8, 128)).astype(np.float16)) for _ in range(2))
+    assert bk.kv_attention_workspace(st.cache, b, 2, 8) > 0
+    alone = [bk.mq_kv_attention(q, st.cache, b) for q in (q1, q2)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(5):
+        torch.cuda._sleep(20000000)                     # some milliseconds
+        o1 = bk.mq_kv_attention(q1, st.cache, b)
+        o2 = bk.mq_kv_attention(q2, st.cache, b, stream=side)
+        side.synchronize()
+        got2 = o2.clone()
+        torch.cuda.synchronize()
+        assert torch.equal(o1, alone[0]) and torch.equal(got2, alone[1])
