@@ -22,7 +22,7 @@ import struct
 
 import torch
 
-from .mosaicq import MQError, STATUS, _check  # noqa: F401  (the errors of both libraries are the same)
+from .mosaicq import MQError, STATUS, _check, _new, _other  # noqa: F401  (the errors of both libraries are the same)
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libmosaicq_block.so")
@@ -100,31 +100,6 @@ def _stream(stream, t) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _other(stream, index: int):
-    """The stream a call is given, where that is not the current one anyway; None else."""
-    if stream is None:
-        return None
-    handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    if handle == _current_stream(index):
-        return None
-    if hasattr(stream, "cuda_stream"):
-        return stream
-    return torch.cuda.ExternalStream(handle, device=index) if handle else torch.cuda.default_stream(index)
-
-
-def _new(other, make, *args):
-    """The new tensor make(*args) for a call on stream `other` (None: the current one). It comes from that stream's
-    pool: the current one's may hand out memory that work queued there still uses. It goes back to that pool only when
-    the current stream is done with it too, where the caller reads it."""
-    if other is None:
-        return make(*args)
-    now = torch.cuda.current_stream(other.device)
-    with torch.cuda.stream(other):
-        t = make(*args)
-    t.record_stream(now)
-    return t
-
-
 def _like(t):
     """A dense tensor of t's shape and type (0.6 us faster than by shape, where t is dense)."""
     return torch.empty_like(t) if t.is_contiguous() else t.new_empty(t.shape)
@@ -166,8 +141,8 @@ class Rope:
         self.rot_dim, self.positions, self.layout = int(rot_dim), int(positions), layout
         spec = _RopeSpec(self.rot_dim, SCALINGS[scaling], theta, factor, original, turns_fast, turns_slow)
         shape = (max(self.positions, 1), max(self.rot_dim // 2, 1), 2)
-        other = None if stream is None else _other(stream, torch.cuda.current_device())
-        self.table = _new(other, lambda: torch.empty(shape, dtype=torch.float32, device="cuda"))
+        other = None if stream is None else _other(stream)
+        self.table = _new(other, torch.empty, shape, dtype=torch.float32, device="cuda")
         _check(lib.mq_rope_table(ctypes.byref(spec), self.positions, self.table.data_ptr(),
                                  _stream(stream, self.table)), "mq_rope_table")
         self._plan = _RopePlan(self.table.data_ptr(), self.positions, self.rot_dim, LAYOUTS[layout])
@@ -185,7 +160,7 @@ def mq_rope(x, rope: Rope, pos, inverse: bool = False, out=None, stream=None):
     T, H, D = x.shape
     _ints(pos, "pos", (T,))
     if out is None:
-        out = _like(x) if stream is None else _new(_other(stream, x.get_device()), _like, x)
+        out = _like(x) if stream is None else _new(_other(stream, x.device), _like, x)
     elif out.dtype is not _F16 or not out.is_cuda or out.shape != x.shape or out.stride(2) != 1:
         raise ValueError("out must be a float16 GPU tensor of x's shape with dense heads")
     if T == 0:
@@ -284,7 +259,7 @@ def mq_kv_append(q, k, v, cache: KVCache, batch: KVBatch, rope: Rope | None = No
         if q is not None:
             Tq, heads, qs = _rows(q, "q", None, D)
             if q_out is None:
-                q_out = _like(q) if stream is None else _new(_other(stream, q.get_device()), _like, q)
+                q_out = _like(q) if stream is None else _new(_other(stream, q.device), _like, q)
                 To, qos = Tq, heads * D
             else:
                 To, _, qos = _rows(q_out, "q_out", heads, D)
@@ -320,7 +295,7 @@ def mq_kv_attention(q, cache: KVCache, batch: KVBatch, causal: bool = True, scal
     Enqueued on `stream` (no sync)."""
     D = cache.head_dim
     T, H, qs = _rows(q, "q", None, D)
-    other = None if stream is None else _other(stream, q.get_device())
+    other = None if stream is None else _other(stream, q.device)
     if out is None:
         out, os_ = _new(other, _like, q), H * D
     else:
@@ -336,7 +311,7 @@ def mq_kv_attention(q, cache: KVCache, batch: KVBatch, causal: bool = True, scal
             raise TypeError("workspace must be a contiguous uint8 tensor on the GPU")
         wp, nw = workspace.data_ptr(), workspace.numel()
     elif need:
-        ws = _new(other, lambda: torch.empty(need, dtype=torch.uint8, device=q.device))
+        ws = _new(other, torch.empty, need, dtype=torch.uint8, device=q.device)
         wp, nw = ws.data_ptr(), need
     code = lib.mq_kv_attention(cache._ref, batch._with(T), q.data_ptr(), H, qs, int(causal),
                                D ** -0.5 if scale is None else scale, out.data_ptr(), os_, wp, nw, _stream(stream, q))
@@ -377,7 +352,7 @@ def mq_norm_residual(y, r, w_pre, w_post=None, gate=None, alpha: float = 1.0, be
         raise ValueError("r must be [tokens, width] with dense rows")
     shape, dt = r.shape, r.dtype
     M, W = shape
-    other = None if stream is None else _other(stream, r.get_device())
+    other = None if stream is None else _other(stream, r.device)
     yp = gp = rp = hp = wpost = wpre = ys = gs = rs = hs = 0
     if y is not None:
         yp, ys = _matrix(y, "y", _F16, shape)

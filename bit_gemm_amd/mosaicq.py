@@ -2,7 +2,8 @@
 
 Argument marshalling only: every step of packing and of the fused linear runs
 in the HIP library. torch tensors supply device memory and the current HIP
-stream. Importing this module fails loudly when the library is not built --
+stream; what a call on another stream makes comes from that stream's memory
+pool. Importing this module fails loudly when the library is not built --
 there is no fallback path.
 """
 from __future__ import annotations
@@ -102,6 +103,33 @@ def _stream_handle(stream):
     if stream is None:
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+
+
+def _other(stream, device=None):
+    """The stream a call is given, where that is not the current one anyway; None else."""
+    if stream is None:
+        return None
+    import torch
+    handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if handle == torch.cuda.current_stream(device).cuda_stream:
+        return None
+    if hasattr(stream, "cuda_stream"):
+        return stream
+    return torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device)
+
+
+def _new(other, make, *args, **kw):
+    """The new tensor make(*args, **kw) for a call on stream `other` (None: the current one). It comes from that stream's
+    pool: the current one's may hand out memory that work queued there still uses. It goes back to that pool only when
+    the current stream is done with it too, where the caller reads it."""
+    if other is None:
+        return make(*args, **kw)
+    import torch
+    now = torch.cuda.current_stream(other.device)
+    with torch.cuda.stream(other):
+        t = make(*args, **kw)
+    t.record_stream(now)
+    return t
 
 
 def _dev_fp16(t, name):
@@ -205,7 +233,7 @@ def mq_pack_blocks(W, group_size: int, block_fraction: float, h, stream=None) ->
     N, K = W.shape
     if not isinstance(h, torch.Tensor) or not h.is_cuda or h.dtype != torch.float32 or tuple(h.shape) != (K,):
         raise TypeError(f"h must be a float32 [{K}] tensor on the GPU")
-    h = h.contiguous()
+    h = h if h.is_contiguous() else _new(_other(stream, W.device), h.contiguous)
     out = ctypes.c_void_p()
     _check(lib.mq_pack_blocks(ptr, N, K, group_size, float(block_fraction), ctypes.c_void_p(h.data_ptr()),
                               _stream_handle(stream), ctypes.byref(out)), "mq_pack_blocks")
@@ -223,9 +251,10 @@ def export_blocks(packed: Packed, stream=None) -> dict:
     nb = ctypes.c_int64()
     _check(lib.mq_block_count(packed.handle, ctypes.byref(nb)), "mq_block_count")
     B = max(nb.value, 0)
-    out = {"blk": torch.empty(max(B, 1), dtype=torch.int32, device="cuda"),
-           "rscale": torch.empty((max(B, 1), 16), dtype=torch.float32, device="cuda"),
-           "rcodes": torch.empty((max(B, 1), 16, 64), dtype=torch.uint8, device="cuda")}
+    other = _other(stream)
+    out = {"blk": _new(other, torch.empty, max(B, 1), dtype=torch.int32, device="cuda"),
+           "rscale": _new(other, torch.empty, (max(B, 1), 16), dtype=torch.float32, device="cuda"),
+           "rcodes": _new(other, torch.empty, (max(B, 1), 16, 64), dtype=torch.uint8, device="cuda")}
     _check(lib.mq_export_blocks(packed.handle, *[ctypes.c_void_p(out[k].data_ptr()) for k in
                                                  ("blk", "rscale", "rcodes")], _stream_handle(stream)),
            "mq_export_blocks")
@@ -242,9 +271,10 @@ def mq_smooth_weights(W, amax_x, stream=None):
     if not isinstance(amax_x, torch.Tensor) or not amax_x.is_cuda or amax_x.dtype != torch.float32 \
             or tuple(amax_x.shape) != (K,):
         raise TypeError(f"amax_x must be a float32 [{K}] tensor on the GPU")
-    amax_x = amax_x.contiguous()
-    Wh = torch.empty_like(W)
-    e = torch.empty(K, dtype=torch.int32, device=W.device)
+    other = _other(stream, W.device)
+    amax_x = amax_x if amax_x.is_contiguous() else _new(other, amax_x.contiguous)
+    Wh = _new(other, torch.empty_like, W)
+    e = _new(other, torch.empty, K, dtype=torch.int32, device=W.device)
     _check(lib.mq_smooth_weights(ptr, N, K, ctypes.c_void_p(amax_x.data_ptr()), ctypes.c_void_p(Wh.data_ptr()),
                                  ctypes.c_void_p(e.data_ptr()), _stream_handle(stream)), "mq_smooth_weights")
     return Wh, e
@@ -257,7 +287,7 @@ def mq_smooth_activations(X, e, out=None, stream=None):
     M, K = X.shape
     if e.dtype != torch.int32 or tuple(e.shape) != (K,) or not e.is_cuda:
         raise TypeError(f"e must be an int32 [{K}] tensor on the GPU")
-    out = torch.empty_like(X) if out is None else out
+    out = _new(_other(stream, X.device), torch.empty_like, X) if out is None else out
     _check(lib.mq_smooth_activations(xp, M, K, ctypes.c_void_p(e.data_ptr()), _dev_fp16(out, "out"),
                                      _stream_handle(stream)), "mq_smooth_activations")
     return out
@@ -274,9 +304,9 @@ def mq_quantize_activations(X, G: int, xq=None, xmeta=None, stream=None):
     M, K = X.shape
     Kp = -(-K // 128) * 128
     if xq is None:
-        xq = torch.empty((M, Kp), dtype=torch.uint8, device=X.device)
+        xq = _new(_other(stream, X.device), torch.empty, (M, Kp), dtype=torch.uint8, device=X.device)
     if xmeta is None:
-        xmeta = torch.empty((M, Kp // G), dtype=torch.int32, device=X.device)
+        xmeta = _new(_other(stream, X.device), torch.empty, (M, Kp // G), dtype=torch.int32, device=X.device)
     if xq.dtype != torch.uint8 or tuple(xq.shape) != (M, Kp) or not xq.is_contiguous():
         raise TypeError(f"xq must be a contiguous uint8 [{M}, {Kp}] tensor")
     if xmeta.dtype != torch.int32 or tuple(xmeta.shape) != (M, Kp // G) or not xmeta.is_contiguous():
@@ -298,7 +328,7 @@ def mq_linear_a4(xq, xmeta, packed: Packed, Y=None, stream=None):
     if xmeta.dtype != torch.int32 or tuple(xmeta.shape) != (M, Kp // packed.G) or not xmeta.is_contiguous():
         raise TypeError(f"xmeta must be a contiguous int32 [M, {Kp // packed.G}] tensor")
     if Y is None:
-        Y = torch.empty((M, packed.N), dtype=torch.float16, device=xq.device)
+        Y = _new(_other(stream, xq.device), torch.empty, (M, packed.N), dtype=torch.float16, device=xq.device)
     yp = _dev_fp16(Y, "Y")
     if tuple(Y.shape) != (M, packed.N):
         raise ValueError(f"Y must be [{M}, {packed.N}]")
@@ -317,7 +347,7 @@ def mq_decode_a4(X, packed: Packed, Y=None, stream=None):
         raise ValueError(f"X must be [M, {packed.K}]")
     M = X.shape[0]
     if Y is None:
-        Y = torch.empty((M, packed.N), dtype=torch.float16, device=X.device)
+        Y = _new(_other(stream, X.device), torch.empty, (M, packed.N), dtype=torch.float16, device=X.device)
     yp = _dev_fp16(Y, "Y")
     if tuple(Y.shape) != (M, packed.N):
         raise ValueError(f"Y must be [{M}, {packed.N}]")
@@ -333,7 +363,7 @@ def mq_linear_with(X, packed: Packed, kernel: int = KERNEL_AUTO, Y=None, stream=
         raise ValueError(f"X must be [M, {packed.K}]")
     M = X.shape[0]
     if Y is None:
-        Y = torch.empty((M, packed.N), dtype=torch.float16, device=X.device)
+        Y = _new(_other(stream, X.device), torch.empty, (M, packed.N), dtype=torch.float16, device=X.device)
     yp = _dev_fp16(Y, "Y")
     if tuple(Y.shape) != (M, packed.N):
         raise ValueError(f"Y must be [{M}, {packed.N}]")
@@ -373,7 +403,9 @@ def mq_linear_group(Xs, packs, Ys=None, stream=None):
         if X.dim() != 2 or tuple(X.shape) != (M, p.K):
             raise ValueError(f"every X must be [{M}, K] of its layer (K = {p.K})")
     if Ys is None:
-        Ys = [torch.empty((M, p.N), dtype=torch.float16, device=Xs[0].device) for p in packs]
+        dev = Xs[0].device
+        other = _other(stream, dev)
+        Ys = [_new(other, torch.empty, (M, p.N), dtype=torch.float16, device=dev) for p in packs]
     Ys = list(Ys)
     if len(Ys) != len(packs):
         raise ValueError("one output per layer")
@@ -432,17 +464,18 @@ def mq_export_canonical(packed: Packed, stream=None, residual: bool = True) -> d
     import torch
     dev = torch.device("cuda", torch.cuda.current_device())
     N, K, G, nnz = packed.N, packed.K, packed.G, packed.nnz
+    other = _other(stream)
     out = {
-        "codes": torch.empty((N, K // 2), dtype=torch.uint8, device=dev),
-        "scales": torch.empty((N, K // G), dtype=torch.float16, device=dev),
+        "codes": _new(other, torch.empty, (N, K // 2), dtype=torch.uint8, device=dev),
+        "scales": _new(other, torch.empty, (N, K // G), dtype=torch.float16, device=dev),
     }
     names = ("codes", "scales", "row_ptr", "col", "rcodes", "rscale")
     if residual:
         out.update({
-            "row_ptr": torch.empty(N + 1, dtype=torch.int32, device=dev),
-            "col": torch.empty(max(nnz, 1), dtype=torch.int16, device=dev),
-            "rcodes": torch.empty(max((nnz + 1) // 2, 1), dtype=torch.uint8, device=dev),
-            "rscale": torch.empty(N, dtype=torch.float32, device=dev),
+            "row_ptr": _new(other, torch.empty, N + 1, dtype=torch.int32, device=dev),
+            "col": _new(other, torch.empty, max(nnz, 1), dtype=torch.int16, device=dev),
+            "rcodes": _new(other, torch.empty, max((nnz + 1) // 2, 1), dtype=torch.uint8, device=dev),
+            "rscale": _new(other, torch.empty, N, dtype=torch.float32, device=dev),
         })
     s = _stream_handle(stream)
     _check(lib.mq_export_canonical(packed.handle, *[ctypes.c_void_p(out[k].data_ptr()) if k in out else None
@@ -460,14 +493,15 @@ def mq_export_tiled(packed: Packed, stream=None) -> dict:
     dev = torch.device("cuda", torch.cuda.current_device())
     Nb = -(-packed.N // 16)
     Kt = -(-packed.K // 128)
-    tiles = torch.empty((Nb, Kt, 64, 16), dtype=torch.uint8, device=dev)
-    tile_ptr = torch.empty(Nb * Kt + 1, dtype=torch.int32, device=dev)
+    other = _other(stream)
+    tiles = _new(other, torch.empty, (Nb, Kt, 64, 16), dtype=torch.uint8, device=dev)
+    tile_ptr = _new(other, torch.empty, Nb * Kt + 1, dtype=torch.int32, device=dev)
     s = _stream_handle(stream)
     _check(lib.mq_export_tiled(packed.handle, ctypes.c_void_p(tiles.data_ptr()),
                                ctypes.c_void_p(tile_ptr.data_ptr()), None, s), "mq_export_tiled")
     torch.cuda.synchronize()
     nstream = int(tile_ptr[-1].item())
-    entries = torch.empty(max(nstream, 1), dtype=torch.int32, device=dev)
+    entries = _new(other, torch.empty, max(nstream, 1), dtype=torch.int32, device=dev)
     _check(lib.mq_export_tiled(packed.handle, None, None, ctypes.c_void_p(entries.data_ptr()), s),
            "mq_export_tiled")
     torch.cuda.synchronize()
