@@ -145,32 +145,39 @@ __global__ __launch_bounds__(THREADS) void k_norm(mq_norm_args a) {
   }
 }
 
+// A launch takes fewer than 2^32 threads: more rows than that run in pieces of 2^31.
+template <typename R, int THREADS, int CH>
+hipError_t go(const mq_norm_args& a, hipStream_t s) {
+  constexpr int64_t step = (int64_t(1) << 31) / THREADS;
+  for (int64_t t = 0; t < a.tokens; t += step) {
+    mq_norm_args p = a;
+    p.tokens = a.tokens - t < step ? a.tokens - t : step;
+    if (a.y) p.y = static_cast<const _Float16*>(a.y) + t * a.y_stride;
+    if (a.gate) p.gate = static_cast<const _Float16*>(a.gate) + t * a.gate_stride;
+    p.r = static_cast<const R*>(a.r) + t * a.r_stride;
+    if (a.y) p.r_out = static_cast<R*>(a.r_out) + t * a.r_out_stride;
+    if (a.w_pre) p.h_out = static_cast<_Float16*>(a.h_out) + t * a.h_stride;
+    k_norm<R, THREADS, CH><<<dim3((unsigned)p.tokens), dim3(THREADS), 0, s>>>(p);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
 template <typename R>
-void dispatch(const mq_norm_args& a, hipStream_t s) {
-  const dim3 g((unsigned)a.tokens);
-  if (a.width <= 2048)
-    k_norm<R, 256, 1><<<g, dim3(256), 0, s>>>(a);
-  else if (a.width <= 4096)
-    k_norm<R, 512, 1><<<g, dim3(512), 0, s>>>(a);
-  else if (a.width <= 8192)
-    k_norm<R, 1024, 1><<<g, dim3(1024), 0, s>>>(a);
-  else if (a.width <= 16384)
-    k_norm<R, 1024, 2><<<g, dim3(1024), 0, s>>>(a);
-  else if (a.width <= 32768)
-    k_norm<R, 1024, 4><<<g, dim3(1024), 0, s>>>(a);
-  else
-    k_norm<R, 1024, 8><<<g, dim3(1024), 0, s>>>(a);
+hipError_t dispatch(const mq_norm_args& a, hipStream_t s) {
+  if (a.width <= 2048) return go<R, 256, 1>(a, s);
+  if (a.width <= 4096) return go<R, 512, 1>(a, s);
+  if (a.width <= 8192) return go<R, 1024, 1>(a, s);
+  if (a.width <= 16384) return go<R, 1024, 2>(a, s);
+  if (a.width <= 32768) return go<R, 1024, 4>(a, s);
+  return go<R, 1024, 8>(a, s);
 }
 
 }  // namespace
 
 hipError_t launch_norm_residual(const mq_norm_args& a, hipStream_t s) {
-  if (a.tokens == 0) return hipSuccess;
-  if (a.residual_fp32)
-    dispatch<float>(a, s);
-  else
-    dispatch<_Float16>(a, s);
-  return hipGetLastError();
+  return a.residual_fp32 ? dispatch<float>(a, s) : dispatch<_Float16>(a, s);
 }
 
 }  // namespace mq

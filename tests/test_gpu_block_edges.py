@@ -239,3 +239,22 @@ def test_attention_on_two_streams_with_work_pending(bk):
         got2 = o2.clone()
         torch.cuda.synchronize()
         assert torch.equal(o1, alone[0]) and torch.equal(got2, alone[1])
+
+
+# ------------------------------------------------------------ large launches
+@pytest.mark.parametrize("f32", [False, True])
+def test_norm_of_more_rows_than_a_launch_has(bk, f32):
+    """2^23 + 3 rows of 256 threads are 2^31 threads and more: the launch is cut, and the rows about the cut are right."""
+    import torch
+    T, W, cut = (1 << 23) + 3, 9, 1 << 23
+    w = torch.ones(W, dtype=torch.float16, device="cuda")
+    r = torch.full((T, W), 2.0, dtype=torch.float32 if f32 else torch.float16, device="cuda")
+    y = torch.full((T, W), 1.0, dtype=torch.float16, device="cuda")
+    g = torch.full((T, W), 0.5, dtype=torch.float16, device="cuda")
+    for t in (0, cut - 1, cut, T - 1):
+        y[t] = torch.arange(W, device="cuda").half()
+    r2, h = bk.mq_norm_residual(y, r, w, gate=g, eps=0.0)
+    want = 2.0 + 0.5 * y.float()
+    assert torch.equal(r2.float(), want)
+    norm = want * (want.square().mean(1, keepdim=True)).rsqrt()
+    assert ((h.float() - norm).abs() <= U * norm + 64 * E * norm).all()
