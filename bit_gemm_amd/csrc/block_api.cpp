@@ -186,7 +186,7 @@ mq_status attention_plan(const mq_kv_cache* cache, const mq_kv_batch* batch, int
   if (q_heads / cache->kv_heads > 64) return MQ_ERR_UNSUPPORTED;
   *plan = mq::plan_attention(cache->kv_heads, q_heads, cache->head_dim, batch->seqs, batch->tokens, batch->max_new,
                              batch->max_len);
-  return plan->groups >= k31 ? MQ_ERR_UNSUPPORTED : MQ_OK;
+  return mq::launchable(plan->groups, plan->threads) && mq::launchable(plan->joins, 256) ? MQ_OK : MQ_ERR_UNSUPPORTED;
 }
 
 }  // namespace

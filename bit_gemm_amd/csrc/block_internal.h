@@ -49,7 +49,7 @@ hipError_t launch_rope_table(const double* freq, int pairs, double mag, int64_t 
 hipError_t launch_rope(const _Float16* x, int64_t tokens, int heads, int dim, int64_t xt, int64_t xh,
                        const int32_t* pos, const RopeView& rope, int inverse, _Float16* y, int64_t yt, int64_t yh,
                        hipStream_t s);
-// grid_too_large: set where the launch would need more than 2^31 - 1 workgroups (nothing is enqueued then)
+// grid_too_large: set where the launch would have too many threads (nothing is enqueued then)
 hipError_t launch_kv_append(const KvView& kv, int dim, int format, const BatchView& b, RowsIn q, int hq, RowsIn k,
                             RowsIn v, const RopeView& rope, RowsOut qo, bool* grid_too_large, hipStream_t s);
 
@@ -59,6 +59,9 @@ hipError_t launch_kv_append(const KvView& kv, int dim, int format, const BatchVi
 constexpr int attn_rows(int dim) { return dim == 64 ? 128 : 256; }
 
 
+// A launch takes fewer than 2^32 threads.
+inline bool launchable(int64_t groups, int threads) { return groups < (int64_t(1) << 32) / threads; }
+
 // How the attention of a batch is run: a rule on sizes alone (kv_attn.hip).
 struct AttnPlan {
   int nt;             // blocks of 16 query rows a workgroup holds; 0: the kernel for many rows, attn_rows of them
@@ -67,6 +70,8 @@ struct AttnPlan {
   int chunk;          // else: cache blocks of one workgroup
   int splits;         // and workgroups along the cache of the longest sequence; 1: no workspace
   int64_t groups;     // workgroups in all
+  int threads;        // of each
+  int64_t joins;      // workgroups of 256 threads that join the splits
   size_t bytes;       // workspace
 };
 AttnPlan plan_attention(int hk, int hq, int dim, int64_t seqs, int64_t tokens, int64_t max_new, int64_t max_len);

@@ -397,7 +397,7 @@ hipError_t launch_kv_append(const KvView& kv, int dim, int format, const BatchVi
   const int64_t q_tokens = 4;
   const int64_t q_groups = rope.table && q.p ? (new_max + q_tokens - 1) / q_tokens : 0;
   const int64_t groups = kv_groups + q_groups * b.seqs;
-  if (groups >= (int64_t(1) << 31)) {
+  if (!launchable(groups, 256)) {
     *grid_too_large = true;
     return hipSuccess;
   }

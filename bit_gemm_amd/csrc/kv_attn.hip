@@ -338,6 +338,10 @@ __global__ __launch_bounds__(256) void k_attn_join(AttnArgs A, int64_t rows) {
 
 int64_t up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// A workgroup of the join has D / 4 threads a row: it takes 8 or 16 rows of up to kFewSplits splits, or one of more.
+constexpr int join_rows(int dim) { return 256 / (dim / 4); }
+constexpr int kFewSplits = 4;
+
 template <int D, int FMT>
 hipError_t go(const AttnArgs& A, const AttnPlan& p, hipStream_t s) {
   const dim3 g((unsigned)p.groups), ts(64 * kWaves), t(256);
@@ -355,11 +359,11 @@ hipError_t go(const AttnArgs& A, const AttnPlan& p, hipStream_t s) {
   }
   if (e != hipSuccess || p.splits == 1) return e;
   const int64_t rows = (int64_t)A.b.tokens * A.hq;
-  constexpr int Y = 256 / (D / 4);   // 8 or 16 groups
-  if (p.splits <= 4)
-    k_attn_join<D, 1><<<dim3((unsigned)up(rows, Y)), t, 0, s>>>(A, rows);
+  const dim3 j((unsigned)p.joins);
+  if (p.splits <= kFewSplits)
+    k_attn_join<D, 1><<<j, t, 0, s>>>(A, rows);
   else
-    k_attn_join<D, Y><<<dim3((unsigned)rows), t, 0, s>>>(A, rows);
+    k_attn_join<D, join_rows(D)><<<j, t, 0, s>>>(A, rows);
   return hipGetLastError();
 }
 
@@ -397,11 +401,13 @@ AttnPlan plan_attention(int hk, int hq, int dim, int64_t seqs, int64_t tokens, i
   p.chunk = (int)up(blocks, splits);
   p.splits = (int)up(blocks, p.chunk);
   p.groups = one * p.splits;
+  p.threads = p.nt > 0 ? 64 * kWaves : 2 * attn_rows(dim);
   if (p.slices) {
     p.groups = 256 * 256 / attn_rows(dim);
     p.bytes = (size_t)p.groups * (2 * attn_rows(dim) * ((size_t)dim * 4 + 8) + sizeof(SlicePart));
     return p;
   }
+  if (p.splits > 1) p.joins = p.splits <= kFewSplits ? up(tokens * hq, join_rows(dim)) : tokens * hq;
   p.bytes = p.splits == 1 ? 0 : (size_t)(tokens * hq) * p.splits * ((size_t)dim * 4 + 8);
   return p;
 }

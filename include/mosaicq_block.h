@@ -163,7 +163,9 @@ typedef struct {
  * gives the same cache while its block is open. Tokens with a negative
  * position, of a block past table_width, or whose block or slot is out of
  * range are dropped. Errors: MQ_ERR_INVALID_ARG, MQ_ERR_UNSUPPORTED (head_dim
- * not 64 or 128, more than 2^31 - 1 tokens or workgroups), MQ_ERR_DEVICE.
+ * not 64 or 128, more than 2^31 - 1 tokens, bounds of 2^24 workgroups or more:
+ * seqs * kv_heads * (max_new + 126) / 64, and seqs * (max_new + 3) / 4 where
+ * queries are turned), MQ_ERR_DEVICE.
  */
 mq_status mq_kv_append(const mq_kv_cache* cache, const mq_kv_batch* batch, const void* q_dev_fp16, int32_t q_heads,
                        int64_t q_stride, const void* k_dev_fp16, int64_t k_stride, const void* v_dev_fp16,
@@ -191,7 +193,9 @@ mq_status mq_kv_append(const mq_kv_cache* cache, const mq_kv_batch* batch, const
  * The same call gives the same bits: work split over a long cache is joined
  * in a fixed order. Errors: MQ_ERR_INVALID_ARG (also a workspace that is too
  * small), MQ_ERR_UNSUPPORTED (head_dim, more than 64 query heads for a kv
- * head, more than 2^31 - 1 workgroups), MQ_ERR_DEVICE.
+ * head, bounds that need 2^32 threads or more: 2 for each of the seqs * kv_heads
+ * * max_new * q_heads / kv_heads rows, 256 for each sequence's kv head at least,
+ * and where a long cache is split 256 for each token's query head), MQ_ERR_DEVICE.
  */
 mq_status mq_kv_attention(const mq_kv_cache* cache, const mq_kv_batch* batch, const void* q_dev_fp16, int32_t q_heads,
                           int64_t q_stride, int32_t causal, float scale, void* out_dev_fp16, int64_t out_stride,
