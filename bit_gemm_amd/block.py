@@ -245,13 +245,15 @@ def mq_kv_append(q, k, v, cache: KVCache, batch: KVBatch, rope: Rope | None = No
     cache. With a rope plan keys are turned to their positions first, and so
     are the queries q [tokens, q_heads, head_dim] (None: no queries), which
     are returned (in q_out where given; it may be q). Without one q is returned
-    as it is. Rows may lie apart (slices of a joined projection). Enqueued on
+    as it is, and there is no q_out. Rows may lie apart (slices of a joined projection). Enqueued on
     `stream` (no sync)."""
     D, hk = cache.head_dim, cache.kv_heads
     T, _, ks = _rows(k, "k", hk, D)
     Tv, _, vs = _rows(v, "v", hk, D)
     if Tv != T:
         raise ValueError("k and v must have the same tokens")
+    if q_out is not None and q_out is not q and (q is None or rope is None):
+        raise ValueError("q_out is written with queries and a rope plan only")
     qp = qo = rp = None
     heads = qs = qos = 0
     if rope is not None:

@@ -193,9 +193,9 @@ mq_status mq_kv_append(const mq_kv_cache* cache, const mq_kv_batch* batch, const
  * The same call gives the same bits: work split over a long cache is joined
  * in a fixed order. Errors: MQ_ERR_INVALID_ARG (also a workspace that is too
  * small), MQ_ERR_UNSUPPORTED (head_dim, more than 64 query heads for a kv
- * head, bounds that need 2^32 threads or more: 2 for each of the seqs * kv_heads
- * * max_new * q_heads / kv_heads rows, 256 for each sequence's kv head at least,
- * and where a long cache is split 256 for each token's query head), MQ_ERR_DEVICE.
+ * head, bounds that need 2^32 threads or more: 2 for each of seqs * max_new *
+ * q_heads rows, 256 for each sequence's kv head at least, and where a long cache
+ * is split 256 for each token's query head), MQ_ERR_DEVICE.
  */
 mq_status mq_kv_attention(const mq_kv_cache* cache, const mq_kv_batch* batch, const void* q_dev_fp16, int32_t q_heads,
                           int64_t q_stride, int32_t causal, float scale, void* out_dev_fp16, int64_t out_stride,
