@@ -62,6 +62,7 @@ class _NormArgs(ctypes.Structure):
 
 # the same fields in their order, packed in a fifth of the time that the structure takes
 _norm_args = struct.Struct("@7P7q4fi4x").pack
+_batch_args = struct.Struct("@4P5q").pack
 
 EXPORTED = ("mq_rope_table", "mq_rope", "mq_kv_append", "mq_kv_attention", "mq_kv_attention_workspace",
             "mq_norm_residual")
@@ -229,15 +230,14 @@ class KVBatch:
         self.block_table = _ints(block_table, "block_table", (S, block_table.shape[1]))
         self.slots = None if slots is None else _ints(slots, "slots", (S,))
         self.seqs, self.max_new, self.max_len = S, int(max_new), int(max_len)
-        self._c = _Batch(cu_q.data_ptr(), kv_len.data_ptr(), block_table.data_ptr(),
-                         None if slots is None else slots.data_ptr(), S, 0, block_table.shape[1], self.max_new,
-                         self.max_len)
-        self._ref = ctypes.addressof(self._c)
+        self._head = (cu_q.data_ptr(), kv_len.data_ptr(), block_table.data_ptr(),
+                      0 if slots is None else slots.data_ptr(), S)
+        self._rest = (block_table.shape[1], self.max_new, self.max_len)
         self._ws = {}      # (tokens, q heads, kv heads, head dim) -> workspace bytes
 
-    def _with(self, tokens: int) -> int:
-        self._c.tokens = tokens
-        return self._ref
+    def _with(self, tokens: int) -> bytes:
+        """The mq_kv_batch of a call of so many tokens: each call's own, since calls may run in several threads."""
+        return _batch_args(*self._head, tokens, *self._rest)
 
 
 def mq_kv_append(q, k, v, cache: KVCache, batch: KVBatch, rope: Rope | None = None, q_out=None, stream=None):

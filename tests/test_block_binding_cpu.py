@@ -44,3 +44,22 @@ def test_append_refuses_an_output_that_it_would_not_write(bk):
     for args, kw in (((q, kv, kv), {}), ((None, kv, kv), {}), ((None, kv, kv), dict(rope=NoPlan()))):
         with pytest.raises(ValueError, match="q_out"):
             bk.mq_kv_append(*args, cache_of(bk), batch_of(bk), q_out=out, **kw)
+
+
+def test_calls_of_one_batch_do_not_share_their_token_count(bk):
+    """Two threads may run calls of one batch with different numbers of tokens: each call's structure is its own."""
+    b = batch_of(bk)
+
+    def tokens(args):
+        p = args if isinstance(args, bytes) else ctypes.string_at(args, ctypes.sizeof(bk._Batch))
+        return bk._Batch.from_buffer_copy(p).tokens
+    two, three = b._with(2), b._with(3)
+    assert (tokens(two), tokens(three)) == (2, 3)
+
+
+def test_batch_arguments_are_packed_as_the_structure_lies(bk):
+    b = batch_of(bk)
+    want = bk._Batch(b.cu_q.data_ptr(), b.kv_len.data_ptr(), b.block_table.data_ptr(), b.slots.data_ptr(), 2, 7, 4, 1, 100)
+    assert b._with(7) == bytes(want)
+    none = bk.KVBatch(b.cu_q, b.kv_len, b.block_table, 1, 100)
+    assert bk._Batch.from_buffer_copy(none._with(7)).slots is None
