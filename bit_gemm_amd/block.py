@@ -9,10 +9,11 @@ decoder block's 4-bit linears.
     r, h = mq_norm_residual(y, r, w_pre)                    # r' = r + y, h = norm(r') w_pre
 
 Argument marshalling only: every step runs in the HIP library, on the given
-stream (the current one by default), without synchronising. What a call makes
-(outputs, workspace) comes from that stream's memory pool; the caller orders
-the streams, and keeps what a call reads until it has run. Importing this
-module fails loudly when the library is not built -- there is no fallback path.
+stream (the current one by default) of its tensors' device, without
+synchronising. What a call makes (outputs, workspace) comes from that stream's
+memory pool; the caller orders the streams, and keeps what a call reads until
+it has run. Importing this module fails loudly when the library is not built --
+there is no fallback path.
 """
 from __future__ import annotations
 
@@ -95,9 +96,12 @@ def _current_stream(index: int) -> int:
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _current_stream)
 
 
-def _stream(stream, t) -> int:
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _stream(stream, device: int) -> int:
     if stream is None:
-        return _current_stream(t.get_device())
+        return _current_stream(device)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -106,12 +110,23 @@ def _like(t):
     return torch.empty_like(t) if t.is_contiguous() else t.new_empty(t.shape)
 
 
-def _rows(t, name: str, heads=None, dim=None):
-    """Checks an fp16 [tokens, heads, dim] GPU tensor whose heads lie dense in a
-    row; gives its tokens, heads and the elements between rows (of at most one
-    row: its own width, whatever its stride says)."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype is not _F16:
-        raise TypeError(f"{name} must be a float16 tensor on the GPU")
+def _device(t, name: str, dt) -> int:
+    """The device of a call's first tensor."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype is not dt:
+        raise TypeError(f"{name} must be a {dt} tensor on the GPU")
+    return t.get_device()
+
+
+def _apart(name: str):
+    return ValueError(f"{name} is on another device than the call's tensors")
+
+
+def _rows(t, name: str, device: int, heads=None, dim=None):
+    """Checks an fp16 [tokens, heads, dim] tensor on the device whose heads lie
+    dense in a row; gives its tokens, heads and the elements between rows (of at
+    most one row: its own width, whatever its stride says)."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != device or t.dtype is not _F16:
+        raise TypeError(f"{name} must be a float16 tensor on GPU {device}")
     if t.dim() != 3 or (heads is not None and t.shape[1] != heads) or (dim is not None and t.shape[2] != dim):
         raise ValueError(f"{name} must be [tokens, {heads or 'heads'}, {dim or 'head dim'}]")
     T, H, D = t.shape
@@ -121,9 +136,9 @@ def _rows(t, name: str, heads=None, dim=None):
     return T, H, st if T > 1 else H * D
 
 
-def _ints(t, name: str, shape):
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype is not torch.int32 or not t.is_contiguous():
-        raise TypeError(f"{name} must be a contiguous int32 tensor on the GPU")
+def _ints(t, name: str, device: int, shape):
+    if not isinstance(t, torch.Tensor) or t.get_device() != device or t.dtype is not torch.int32 or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous int32 tensor on GPU {device}")
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must be {list(shape)}")
     return t
@@ -144,8 +159,9 @@ class Rope:
         shape = (max(self.positions, 1), max(self.rot_dim // 2, 1), 2)
         other = None if stream is None else _other(stream)
         self.table = _new(other, torch.empty, shape, dtype=torch.float32, device="cuda")
+        self.device = self.table.get_device()
         _check(lib.mq_rope_table(ctypes.byref(spec), self.positions, self.table.data_ptr(),
-                                 _stream(stream, self.table)), "mq_rope_table")
+                                 _stream(stream, self.device)), "mq_rope_table")
         self._plan = _RopePlan(self.table.data_ptr(), self.positions, self.rot_dim, LAYOUTS[layout])
         self._ref = ctypes.addressof(self._plan)
 
@@ -154,22 +170,27 @@ def mq_rope(x, rope: Rope, pos, inverse: bool = False, out=None, stream=None):
     """x [tokens, heads, head_dim] with its heads turned to positions pos
     [tokens] int32 (turned back with inverse); out may be x. Enqueued on
     `stream` (no sync)."""
-    if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dtype is not _F16:
-        raise TypeError("x must be a float16 tensor on the GPU")
+    device = _device(x, "x", _F16)
+    if rope.device != device:
+        raise _apart("rope")
     if x.dim() != 3 or x.stride(2) != 1:
         raise ValueError("x must be [tokens, heads, head_dim] with dense heads")
     T, H, D = x.shape
-    _ints(pos, "pos", (T,))
+    _ints(pos, "pos", device, (T,))
+    if out is not None and (out.dtype is not _F16 or out.get_device() != device or out.shape != x.shape or
+                            out.stride(2) != 1):
+        raise ValueError("out must be a float16 tensor of x's shape with dense heads, on x's device")
+    if device != _current_device():
+        with torch.cuda.device(device):
+            return mq_rope(x, rope, pos, inverse, out, stream)
     if out is None:
         out = _like(x) if stream is None else _new(_other(stream, x.device), _like, x)
-    elif out.dtype is not _F16 or not out.is_cuda or out.shape != x.shape or out.stride(2) != 1:
-        raise ValueError("out must be a float16 GPU tensor of x's shape with dense heads")
     if T == 0:
         return out
     xt, xh, _ = x.stride()
     yt, yh, _ = out.stride()
     code = lib.mq_rope(x.data_ptr(), T, H, D, xt, xh, pos.data_ptr(), rope._ref, int(inverse), out.data_ptr(), yt, yh,
-                       _stream(stream, x))
+                       _stream(stream, device))
     if code:
         raise MQError(code, "mq_rope")
     return out
@@ -194,11 +215,14 @@ class KVCache:
         for name, (t, dt, shape) in want.items():
             if not t.is_cuda or t.dtype is not dt or not t.is_contiguous():
                 raise TypeError(f"{name} must be a contiguous {dt} tensor on the GPU")
+            if t.get_device() != k_codes.get_device():
+                raise ValueError(f"{name} must be on the device of k_codes")
             if tuple(t.shape) != shape:
                 raise ValueError(f"{name} must be {list(shape)}")
         self.k_codes, self.v_codes, self.k_scale, self.v_scale = k_codes, v_codes, k_scale, v_scale
         self.k_tail, self.v_tail = k_tail, v_tail
         self.num_blocks, self.num_slots, self.kv_heads, self.head_dim = nb, ns, hk, D
+        self.device = k_codes.get_device()
         self._c = _Cache(*[t.data_ptr() for t in (k_codes, v_codes, k_scale, v_scale, k_tail, v_tail)], nb, ns, hk, D,
                          FORMATS[k_codes.dtype])
         self._ref = ctypes.addressof(self._c)
@@ -224,11 +248,12 @@ class KVBatch:
 
     def __init__(self, cu_q, kv_len, block_table, max_new: int, max_len: int, slots=None):
         S = kv_len.shape[0]
-        self.cu_q, self.kv_len = _ints(cu_q, "cu_q", (S + 1,)), _ints(kv_len, "kv_len", (S,))
+        self.device = _device(cu_q, "cu_q", torch.int32)
+        self.cu_q, self.kv_len = _ints(cu_q, "cu_q", self.device, (S + 1,)), _ints(kv_len, "kv_len", self.device, (S,))
         if block_table.dim() != 2:
             raise ValueError("block_table must be [seqs, width]")
-        self.block_table = _ints(block_table, "block_table", (S, block_table.shape[1]))
-        self.slots = None if slots is None else _ints(slots, "slots", (S,))
+        self.block_table = _ints(block_table, "block_table", self.device, (S, block_table.shape[1]))
+        self.slots = None if slots is None else _ints(slots, "slots", self.device, (S,))
         self.seqs, self.max_new, self.max_len = S, int(max_new), int(max_len)
         self._head = (cu_q.data_ptr(), kv_len.data_ptr(), block_table.data_ptr(),
                       0 if slots is None else slots.data_ptr(), S)
@@ -245,11 +270,13 @@ def mq_kv_append(q, k, v, cache: KVCache, batch: KVBatch, rope: Rope | None = No
     cache. With a rope plan keys are turned to their positions first, and so
     are the queries q [tokens, q_heads, head_dim] (None: no queries), which
     are returned (in q_out where given; it may be q). Without one q is returned
-    as it is, and there is no q_out. Rows may lie apart (slices of a joined projection). Enqueued on
-    `stream` (no sync)."""
-    D, hk = cache.head_dim, cache.kv_heads
-    T, _, ks = _rows(k, "k", hk, D)
-    Tv, _, vs = _rows(v, "v", hk, D)
+    as it is, and there is no q_out. Rows may lie apart (slices of a joined
+    projection). Enqueued on `stream` (no sync)."""
+    D, hk, device = cache.head_dim, cache.kv_heads, cache.device
+    T, _, ks = _rows(k, "k", device, hk, D)
+    Tv, _, vs = _rows(v, "v", device, hk, D)
+    if batch.device != device:
+        raise _apart("batch")
     if Tv != T:
         raise ValueError("k and v must have the same tokens")
     if q_out is not None and q_out is not q and (q is None or rope is None):
@@ -257,20 +284,24 @@ def mq_kv_append(q, k, v, cache: KVCache, batch: KVBatch, rope: Rope | None = No
     qp = qo = rp = None
     heads = qs = qos = 0
     if rope is not None:
+        if rope.device != device:
+            raise _apart("rope")
         rp = rope._ref
         if q is not None:
-            Tq, heads, qs = _rows(q, "q", None, D)
-            if q_out is None:
-                q_out = _like(q) if stream is None else _new(_other(stream, q.device), _like, q)
-                To, qos = Tq, heads * D
-            else:
-                To, _, qos = _rows(q_out, "q_out", heads, D)
+            Tq, heads, qs = _rows(q, "q", device, None, D)
+            To, _, qos = _rows(q_out, "q_out", device, heads, D) if q_out is not None else (Tq, heads, heads * D)
             if Tq != T or To != T:
                 raise ValueError("q, q_out, k and v must have the same tokens")
-            qp, qo = q.data_ptr(), q_out.data_ptr()
+    if device != _current_device():
+        with torch.cuda.device(device):
+            return mq_kv_append(q, k, v, cache, batch, rope, q_out, stream)
+    if heads:
+        if q_out is None:
+            q_out = _like(q) if stream is None else _new(_other(stream, q.device), _like, q)
+        qp, qo = q.data_ptr(), q_out.data_ptr()
     if T:
         code = lib.mq_kv_append(cache._ref, batch._with(T), qp, heads, qs, k.data_ptr(), ks, v.data_ptr(), vs, rp, qo,
-                                qos, _stream(stream, k))
+                                qos, _stream(stream, device))
         if code:
             raise MQError(code, "mq_kv_append")
     return q if qo is None else q_out
@@ -295,46 +326,54 @@ def mq_kv_attention(q, cache: KVCache, batch: KVBatch, causal: bool = True, scal
     sequence's end, or over all cached tokens. workspace: a uint8 GPU tensor of
     at least kv_attention_workspace bytes (None: taken from torch's allocator).
     Enqueued on `stream` (no sync)."""
-    D = cache.head_dim
-    T, H, qs = _rows(q, "q", None, D)
-    other = None if stream is None else _other(stream, q.device)
-    if out is None:
-        out, os_ = _new(other, _like, q), H * D
-    else:
-        To, _, os_ = _rows(out, "out", H, D)
+    D, device = cache.head_dim, cache.device
+    T, H, qs = _rows(q, "q", device, None, D)
+    if batch.device != device:
+        raise _apart("batch")
+    os_ = H * D
+    if out is not None:
+        To, _, os_ = _rows(out, "out", device, H, D)
         if To != T:
             raise ValueError("out must have q's tokens")
+    if workspace is not None and (workspace.dtype is not torch.uint8 or workspace.get_device() != device or
+                                  not workspace.is_contiguous()):
+        raise TypeError(f"workspace must be a contiguous uint8 tensor on GPU {device}")
+    if device != _current_device():
+        with torch.cuda.device(device):
+            return mq_kv_attention(q, cache, batch, causal, scale, out, workspace, stream)
+    other = None if stream is None else _other(stream, q.device)
+    if out is None:
+        out = _new(other, _like, q)
     if T == 0:
         return out
     need = kv_attention_workspace(cache, batch, T, H)
     wp, nw = None, 0
     if workspace is not None:
-        if workspace.dtype is not torch.uint8 or not workspace.is_cuda or not workspace.is_contiguous():
-            raise TypeError("workspace must be a contiguous uint8 tensor on the GPU")
         wp, nw = workspace.data_ptr(), workspace.numel()
     elif need:
         ws = _new(other, torch.empty, need, dtype=torch.uint8, device=q.device)
         wp, nw = ws.data_ptr(), need
     code = lib.mq_kv_attention(cache._ref, batch._with(T), q.data_ptr(), H, qs, int(causal),
-                               D ** -0.5 if scale is None else scale, out.data_ptr(), os_, wp, nw, _stream(stream, q))
+                               D ** -0.5 if scale is None else scale, out.data_ptr(), os_, wp, nw,
+                               _stream(stream, device))
     if code:
         raise MQError(code, "mq_kv_attention")
     return out
 
 
-def _matrix(t, name: str, dt, shape):
-    """Address and row stride of a [tokens, width] GPU tensor with dense rows."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype is not dt:
-        raise TypeError(f"{name} must be a {dt} tensor on the GPU")
+def _matrix(t, name: str, device: int, dt, shape):
+    """Address and row stride of a [tokens, width] tensor on the device with dense rows."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != device or t.dtype is not dt:
+        raise TypeError(f"{name} must be a {dt} tensor on GPU {device}")
     st = t.stride()
     if t.shape != shape or st[1] != 1:
         raise ValueError(f"{name} must be {list(shape)} with dense rows")
     return t.data_ptr(), st[0] if shape[0] > 1 else shape[1]
 
 
-def _vector(t, name: str, width: int):
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype is not _F16 or not t.is_contiguous():
-        raise TypeError(f"{name} must be a contiguous float16 tensor on the GPU")
+def _vector(t, name: str, device: int, width: int):
+    if not isinstance(t, torch.Tensor) or t.get_device() != device or t.dtype is not _F16 or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous float16 tensor on GPU {device}")
     if t.dim() != 1 or t.shape[0] != width:
         raise ValueError(f"{name} must be [{width}]")
     return t.data_ptr()
@@ -350,6 +389,10 @@ def mq_norm_residual(y, r, w_pre, w_post=None, gate=None, alpha: float = 1.0, be
     sync)."""
     if not isinstance(r, torch.Tensor) or not r.is_cuda or r.dtype not in (_F16, torch.float32):
         raise TypeError("r must be a float16 or float32 tensor on the GPU")
+    device = r.get_device()
+    if device != _current_device():
+        with torch.cuda.device(device):
+            return mq_norm_residual(y, r, w_pre, w_post, gate, alpha, beta, eps, weight_offset, r_out, h_out, stream)
     if r.dim() != 2 or r.stride(1) != 1:
         raise ValueError("r must be [tokens, width] with dense rows")
     shape, dt = r.shape, r.dtype
@@ -357,35 +400,35 @@ def mq_norm_residual(y, r, w_pre, w_post=None, gate=None, alpha: float = 1.0, be
     other = None if stream is None else _other(stream, r.device)
     yp = gp = rp = hp = wpost = wpre = ys = gs = rs = hs = 0
     if y is not None:
-        yp, ys = _matrix(y, "y", _F16, shape)
+        yp, ys = _matrix(y, "y", device, _F16, shape)
         if r_out is None:
             r_out = _new(other, _like, r)
             rp, rs = r_out.data_ptr(), W
         else:
-            rp, rs = _matrix(r_out, "r_out", dt, shape)
+            rp, rs = _matrix(r_out, "r_out", device, dt, shape)
         if w_post is not None:
-            wpost = _vector(w_post, "w_post", W)
+            wpost = _vector(w_post, "w_post", device, W)
         if gate is not None:
             if gate.dim() == 1:
-                gp = _vector(gate, "gate", W)
+                gp = _vector(gate, "gate", device, W)
             else:
-                gp, gs = _matrix(gate, "gate", _F16, shape)
+                gp, gs = _matrix(gate, "gate", device, _F16, shape)
     else:
         r_out = r
     if w_pre is not None:
-        wpre = _vector(w_pre, "w_pre", W)
+        wpre = _vector(w_pre, "w_pre", device, W)
         if h_out is None:
             h_out = _new(other, w_pre.new_empty, shape) if y is None else _new(other, _like, y)
             hp, hs = h_out.data_ptr(), W
         else:
-            hp, hs = _matrix(h_out, "h_out", _F16, shape)
+            hp, hs = _matrix(h_out, "h_out", device, _F16, shape)
     else:
         h_out = None
     if M == 0:
         return r_out, h_out
     a = _norm_args(yp, r.data_ptr(), gp, wpost, wpre, rp, hp, M, W, ys, r.stride(0) if M > 1 else W, gs, rs, hs, alpha,
                    beta, eps, weight_offset, dt is not _F16)
-    code = lib.mq_norm_residual(a, _stream(stream, r))
+    code = lib.mq_norm_residual(a, _stream(stream, device))
     if code:
         raise MQError(code, "mq_norm_residual")
     return r_out, h_out
