@@ -101,8 +101,9 @@ mq_status mq_rope(const void* X_dev_fp16, int64_t tokens, int32_t heads, int32_t
  * Tokens are cached in blocks of 64. A block that is full holds 8-bit codes
  * with one fp32 scale for each kv head, of its keys and of its values:
  *   scale = max |x| / M over the head's 64 x head_dim elements, M = 127 (int8)
- *   or 448 (OCP e4m3); code = round to nearest even of x (M / max |x|), whole
- *   numbers clamped to -127 .. 127 or e4m3; all 0 where max |x| = 0.
+ *   or 448 (OCP e4m3); code = round to nearest even of x i, whole numbers clamped
+ *   to -127 .. 127 or e4m3, with i = M (1 / max |x|), each of these fp32 steps
+ *   rounded; all 0 where max |x| = 0.
  * A sequence's last block, while it is not full, stays in fp16 in the
  * sequence's slot of the tails, and is coded once, when its last token
  * arrives: codes do not depend on how the tokens arrived, and no code is
