@@ -258,3 +258,42 @@ def test_norm_of_more_rows_than_a_launch_has(bk, f32):
     assert torch.equal(r2.float(), want)
     norm = want * (want.square().mean(1, keepdim=True)).rsqrt()
     assert ((h.float() - norm).abs() <= U * norm + 64 * E * norm).all()
+
+
+# ------------------------------------- whole turns of the kernel for many rows
+@pytest.mark.parametrize("new,lens,hk,D", [([130, 300], [1000, 1700], 2, 64), ([100, 200], [1300, 700], 2, 128),
+                                           ([130, 300], [900, 950], 2, 128), ([120, 200], [900, 1200], 32, 64)])
+def test_bad_blocks_in_the_middle_of_a_prompt(bk, new, lens, hk, D):
+    """A vector that is not finite, and a block that does not exist, among whole blocks far from a sequence's end: NaN for
+    every row of that head (of every head) and for no other."""
+    import torch
+    hq = 2 * hk
+    st = Setup(bk, lens, hk, D, "e4m3", seed=D)
+    st.fill()
+    q = dev(st.g.standard_normal((sum(new), hq, D)).astype(np.float16))
+    good = bk.mq_kv_attention(q, st.cache, st.batch(new))
+    assert good.isfinite().all()
+    st.cache.k_scale[st.tables[0][3], 1] = float("nan")     # what the append leaves for such a vector
+    got = bk.mq_kv_attention(q, st.cache, st.batch(new))
+    bad = torch.zeros(q.shape[:2], dtype=torch.bool, device="cuda")
+    bad[:new[0], 2:4] = True
+    assert got[bad].isnan().all() and torch.equal(got[~bad], good[~bad])
+    for missing in (st.cache.num_blocks, -1):
+        st.table[1, 4] = missing
+        got = bk.mq_kv_attention(q, st.cache, st.batch(new))
+        bad[new[0]:] = True
+        assert got[bad].isnan().all() and torch.equal(got[~bad], good[~bad])
+
+
+@pytest.mark.parametrize("new,lens,hq,hk,D", [([1, 1], [2000, 70], 4, 2, 128), ([90, 40], [1500, 700], 4, 2, 64),
+                                              ([100], [3000], 4, 2, 128), ([70, 200], [900, 1100], 64, 32, 64)])
+def test_attention_under_wide_bounds(bk, new, lens, hq, hk, D):
+    """max_new and max_len far above what there is: every row within the tolerance of the oracle."""
+    st = Setup(bk, lens, hk, D, "int8", seed=13)
+    st.fill()
+    q = dev(st.g.standard_normal((sum(new), hq, D)).astype(np.float16))
+    b = st.batch(new)
+    rows = [0, 1, 31, 39, 64, 89, 99, 128, 199]
+    for more, longer in ((1, 8), (3, 1), (5, 30)):
+        other = bk.KVBatch(b.cu_q, b.kv_len, b.block_table, b.max_new * more, b.max_len * longer, slots=b.slots)
+        check_attention(st, q, new, True, rows=rows, batch=other)
