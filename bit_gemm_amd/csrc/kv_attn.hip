@@ -28,8 +28,8 @@
 // The waves' results are joined in LDS in wave order. Where the sequences do
 // not fill the GPU, the cache is split over workgroups, whose partial results
 // go to the workspace and are joined in a fixed order by k_attn_join.
-// Heads of 128: 16 tokens of 500 to 4096 cached ones, 32 kv heads (282 MB): 52 us,
-// 5.4 TB/s; 2 of 65500, 8 kv heads (267 MB): 42 us, 6.3 TB/s, and 4.5 us to join;
+// Heads of 128: 16 tokens of 500 to 4096 cached ones, 32 kv heads (282 MB): 51 us,
+// 5.5 TB/s; 2 of 65500, 8 kv heads (267 MB): 41 us, 6.5 TB/s, and 4.7 us to join;
 // one of 300: 8 us, of which 4 are the launch and the chain of its loads.
 #include <algorithm>
 

@@ -25,7 +25,7 @@
 // workgroup takes 1.88 us with heads of 128 (all the GPU: 1.1 PFLOP/s, what a large
 // product of matrices reaches) and 1.3 us with heads of 64 (0.8; the exponentials
 // are as many for half the products). With their starts, ends and the blocks on the
-// diagonal: a prompt of 4096, 32 query and 8 kv heads of 128 (137 GFLOP): 143 us.
+// diagonal: a prompt of 4096, 32 query and 8 kv heads of 128 (137 GFLOP): 142 us.
 #include <type_traits>
 
 #include "kv_attn_common.h"

@@ -8,7 +8,7 @@
 // r'^2, in fp32, a thread's own elements first, then the lanes of a wave, then
 // the waves in order. Bound by HBM for many rows (y, r, gate read, r', h
 // written); by the two dependent sums and the load before them for few. 4096
-// rows of 8192, fp32 residual and a gate (470 MB): 88 us, 5.3 TB/s, the rate of
+// rows of 8192, fp32 residual and a gate (470 MB): 87 us, 5.4 TB/s, the rate of
 // a large copy; 16 rows of 4096: 4.3 us. Rows past 32768 elements spill.
 #include "block_common.h"
 

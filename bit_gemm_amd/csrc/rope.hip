@@ -4,8 +4,8 @@
 // y_a = x_a c - x_b s, y_b = x_b c + x_a s for each pair (a, b) of a head.
 // Bound by HBM: 4 bytes an element (read and written once) and 8 bytes of
 // table for each pair of a token, which all of its heads share. 8192 tokens of
-// 64 heads of 128, half of each turned (271 MB): 51 us, 5.3 TB/s, the rate of a
-// large copy. 16 tokens of 32 heads: 3.2 us, the launch and two dependent loads.
+// 64 heads of 128, half of each turned (271 MB): 50 us, 5.4 TB/s, the rate of a
+// large copy. 16 tokens of 32 heads: 3.0 us, the launch and two dependent loads.
 #include <algorithm>
 
 #include "block_common.h"
