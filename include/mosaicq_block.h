@@ -86,8 +86,8 @@ typedef struct {
  *   inverse      0, or 1 to turn back (the transpose, which is also the
  *                gradient; where the scaling has m != 1, m multiplies again)
  *   Y_dev_fp16   as X with its own strides; Y may be X with X's strides
- *   tokens >= 0 (0 enqueues nothing), heads >= 1, head_dim >= 2; pointers
- *   2-byte aligned
+ *   tokens >= 0 (0 enqueues nothing; arguments are checked all the same), heads
+ *   >= 1, head_dim >= 2; pointers not NULL, 2-byte aligned
  *
  * Products and sums are rounded one by one in fp32, the result once to fp16.
  * Errors: MQ_ERR_INVALID_ARG, MQ_ERR_UNSUPPORTED (tokens or heads * head_dim
