@@ -113,7 +113,7 @@ def _other(stream, device=None):
     handle = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
     if handle == torch.cuda.current_stream(device).cuda_stream:
         return None
-    if hasattr(stream, "cuda_stream"):
+    if isinstance(stream, torch.cuda.Stream):
         return stream
     return torch.cuda.ExternalStream(handle, device) if handle else torch.cuda.default_stream(device)
 

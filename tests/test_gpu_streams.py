@@ -51,3 +51,21 @@ def test_outputs_on_another_stream_are_not_the_current_ones_memory(raw):
         side.synchronize()
         assert all(t.data_ptr() not in block for t in got), name
         assert all(torch.equal(a, b) for a, b in zip(got, want)), name
+
+
+def test_any_object_with_a_stream_handle_is_taken():
+    """A stream of another library, which is known by its cuda_stream alone."""
+    import torch
+    mq = require_gpu()
+
+    class Handle:
+        def __init__(self, stream):
+            self.stream, self.cuda_stream = stream, stream.cuda_stream
+    W = to_dev((np.random.default_rng(3).standard_normal((64, 128)) * 0.02).astype(np.float16))
+    X = to_dev(np.random.default_rng(4).standard_normal((3, 128)).astype(np.float16))
+    p = mq.mq_pack(W, 128, 0.0)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    y = mq.mq_linear(X, p, stream=Handle(side))
+    side.synchronize()
+    assert torch.equal(y, mq.mq_linear(X, p))
