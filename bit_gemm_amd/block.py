@@ -7,6 +7,7 @@ decoder block's 4-bit linears.
     q = mq_kv_append(q, k, v, cache, batch, rope=rope)      # rotates q and k, writes k and v
     o = mq_kv_attention(q, cache, batch)
     r, h = mq_norm_residual(y, r, w_pre)                    # r' = r + y, h = norm(r') w_pre
+    r, codes, scales = mq_norm_residual_q8(y, r, w_pre)     # h as 8-bit rows, for head.mq_linear8
 
 Argument marshalling only: every step runs in the HIP library, on the given
 stream (the current one by default) of its tensors' device, without
@@ -66,7 +67,7 @@ _norm_args = struct.Struct("@7P7q4fi4x").pack
 _batch_args = struct.Struct("@4P5q").pack
 
 EXPORTED = ("mq_rope_table", "mq_rope", "mq_kv_append", "mq_kv_attention", "mq_kv_attention_workspace",
-            "mq_norm_residual")
+            "mq_norm_residual", "mq_norm_residual_q8")
 
 
 def _load():
@@ -79,6 +80,7 @@ def _load():
     lib.mq_kv_attention_workspace.argtypes = [_vp, _vp, _i32, _vp]
     lib.mq_kv_attention.argtypes = [_vp, _vp, _vp, _i32, _i64, _i32, _f32, _vp, _i64, _vp, ctypes.c_size_t, _vp]
     lib.mq_norm_residual.argtypes = [_vp, _vp]
+    lib.mq_norm_residual_q8.argtypes = [_vp, _vp, _i64, _vp]
     for name in EXPORTED:
         getattr(lib, name).restype = ctypes.c_int
     return lib
@@ -379,6 +381,26 @@ def _vector(t, name: str, device: int, width: int):
     return t.data_ptr()
 
 
+def _branch(y, r, w_post, gate, r_out, other, device: int, shape, dt):
+    """Addresses and strides of a norm's branch: y, w_post, gate and r_out, which is made where it is not given."""
+    M, W = shape
+    yp, ys = _matrix(y, "y", device, _F16, shape)
+    wpost = gp = gs = 0
+    if r_out is None:
+        r_out = _new(other, _like, r)
+        rp, rs = r_out.data_ptr(), W
+    else:
+        rp, rs = _matrix(r_out, "r_out", device, dt, shape)
+    if w_post is not None:
+        wpost = _vector(w_post, "w_post", device, W)
+    if gate is not None:
+        if gate.dim() == 1:
+            gp = _vector(gate, "gate", device, W)
+        else:
+            gp, gs = _matrix(gate, "gate", device, _F16, shape)
+    return yp, ys, wpost, gp, gs, r_out, rp, rs
+
+
 def mq_norm_residual(y, r, w_pre, w_post=None, gate=None, alpha: float = 1.0, beta: float = 1.0, eps: float = 1e-6,
                      weight_offset: float = 0.0, r_out=None, h_out=None, stream=None):
     """(r', h): r' = alpha r + beta gate N(y) and h = norm(r') (w_pre + offset),
@@ -400,19 +422,7 @@ def mq_norm_residual(y, r, w_pre, w_post=None, gate=None, alpha: float = 1.0, be
     other = None if stream is None else _other(stream, r.device)
     yp = gp = rp = hp = wpost = wpre = ys = gs = rs = hs = 0
     if y is not None:
-        yp, ys = _matrix(y, "y", device, _F16, shape)
-        if r_out is None:
-            r_out = _new(other, _like, r)
-            rp, rs = r_out.data_ptr(), W
-        else:
-            rp, rs = _matrix(r_out, "r_out", device, dt, shape)
-        if w_post is not None:
-            wpost = _vector(w_post, "w_post", device, W)
-        if gate is not None:
-            if gate.dim() == 1:
-                gp = _vector(gate, "gate", device, W)
-            else:
-                gp, gs = _matrix(gate, "gate", device, _F16, shape)
+        yp, ys, wpost, gp, gs, r_out, rp, rs = _branch(y, r, w_post, gate, r_out, other, device, shape, dt)
     else:
         r_out = r
     if w_pre is not None:
@@ -432,3 +442,54 @@ def mq_norm_residual(y, r, w_pre, w_post=None, gate=None, alpha: float = 1.0, be
     if code:
         raise MQError(code, "mq_norm_residual")
     return r_out, h_out
+
+
+_E4M3, _E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
+
+
+def _rows8(codes, scales, device: int, tokens: int, width: int):
+    """Checks the 8-bit rows of [tokens, width]: codes float8_e4m3fn [tokens, 128 n], scales float8_e8m0fnu [tokens, n],
+    n = ceil(width / 128), rows dense. Addresses and strides."""
+    n = (width + 127) // 128
+    cp, cs = _matrix(codes, "codes", device, _E4M3, (tokens, 128 * n))
+    sp, ss = _matrix(scales, "scales", device, _E8M0, (tokens, n))
+    return cp, cs, sp, ss
+
+
+def mq_norm_residual_q8(y, r, w_pre, w_post=None, gate=None, alpha: float = 1.0, beta: float = 1.0, eps: float = 1e-6,
+                        weight_offset: float = 0.0, r_out=None, codes_out=None, scales_out=None, stream=None):
+    """(r', codes, scales): mq_norm_residual with h = norm(r') (w_pre + offset) as 8-bit rows, for head.mq_linear8.
+    codes float8_e4m3fn [tokens, 128 n] and scales float8_e8m0fnu [tokens, n], n = ceil(width / 128): a power of two
+    for each block of 128 elements, zeros past width. Enqueued on `stream` (no sync)."""
+    if not isinstance(r, torch.Tensor) or not r.is_cuda or r.dtype not in (_F16, torch.float32):
+        raise TypeError("r must be a float16 or float32 tensor on the GPU")
+    device = r.get_device()
+    if device != _current_device():
+        with torch.cuda.device(device):
+            return mq_norm_residual_q8(y, r, w_pre, w_post, gate, alpha, beta, eps, weight_offset, r_out, codes_out,
+                                       scales_out, stream)
+    if r.dim() != 2 or r.stride(1) != 1:
+        raise ValueError("r must be [tokens, width] with dense rows")
+    shape, dt = r.shape, r.dtype
+    M, W = shape
+    other = None if stream is None else _other(stream, r.device)
+    yp = gp = rp = wpost = ys = gs = rs = 0
+    if y is not None:
+        yp, ys, wpost, gp, gs, r_out, rp, rs = _branch(y, r, w_post, gate, r_out, other, device, shape, dt)
+    else:
+        r_out = r
+    wpre = _vector(w_pre, "w_pre", device, W)
+    n = (W + 127) // 128
+    if codes_out is None:
+        codes_out = _new(other, torch.empty, (M, 128 * n), dtype=_E4M3, device=r.device)
+    if scales_out is None:
+        scales_out = _new(other, torch.empty, (M, n), dtype=_E8M0, device=r.device)
+    cp, cs, sp, ss = _rows8(codes_out, scales_out, device, M, W)
+    if M == 0:
+        return r_out, codes_out, scales_out
+    a = _norm_args(yp, r.data_ptr(), gp, wpost, wpre, rp, cp, M, W, ys, r.stride(0) if M > 1 else W, gs, rs, cs, alpha,
+                   beta, eps, weight_offset, dt is not _F16)
+    code = lib.mq_norm_residual_q8(a, sp, ss, _stream(stream, device))
+    if code:
+        raise MQError(code, "mq_norm_residual_q8")
+    return r_out, codes_out, scales_out

@@ -221,9 +221,10 @@ MQ_API mq_status mq_kv_attention(const mq_kv_cache* cache, const mq_kv_batch* ba
                                           static_cast<hipStream_t>(hip_stream)));
 }
 
-MQ_API mq_status mq_norm_residual(const mq_norm_args* args, void* hip_stream) {
-  if (!args) return MQ_ERR_INVALID_ARG;
-  const mq_norm_args& a = *args;
+namespace {
+
+// What the norms check alike; all but their h.
+mq_status check_norm(const mq_norm_args& a) {
   if (a.tokens < 0 || a.width <= 0 || !a.r || (!a.y && !a.w_pre)) return MQ_ERR_INVALID_ARG;
   if (a.residual_fp32 != 0 && a.residual_fp32 != 1) return MQ_ERR_INVALID_ARG;
   const size_t rs = a.residual_fp32 ? 4 : 2;
@@ -235,8 +236,39 @@ MQ_API mq_status mq_norm_residual(const mq_norm_args* args, void* hip_stream) {
     if (!std::isfinite(a.alpha) || !std::isfinite(a.beta)) return MQ_ERR_INVALID_ARG;
   }
   if (!aligned(a.w_post, 2) || !aligned(a.w_pre, 2)) return MQ_ERR_INVALID_ARG;
-  if (a.w_pre && bad_rows(a.h_out, a.h_stride, a.width)) return MQ_ERR_INVALID_ARG;
+  return MQ_OK;
+}
+
+mq_status check_norm_rest(const mq_norm_args& a) {
   if (!(a.eps >= 0.0f) || !std::isfinite(a.eps) || !std::isfinite(a.weight_offset)) return MQ_ERR_INVALID_ARG;
   if (a.width > 65536 || a.tokens >= k31) return MQ_ERR_UNSUPPORTED;
+  return MQ_OK;
+}
+
+}  // namespace
+
+MQ_API mq_status mq_norm_residual(const mq_norm_args* args, void* hip_stream) {
+  if (!args) return MQ_ERR_INVALID_ARG;
+  const mq_norm_args& a = *args;
+  mq_status st = check_norm(a);
+  if (st != MQ_OK) return st;
+  if (a.w_pre && bad_rows(a.h_out, a.h_stride, a.width)) return MQ_ERR_INVALID_ARG;
+  st = check_norm_rest(a);
+  if (st != MQ_OK) return st;
   return from_hip(mq::launch_norm_residual(a, static_cast<hipStream_t>(hip_stream)));
+}
+
+MQ_API mq_status mq_norm_residual_q8(const mq_norm_args* args, void* scales_dev, int64_t scales_stride,
+                                     void* hip_stream) {
+  if (!args || !args->w_pre) return MQ_ERR_INVALID_ARG;
+  const mq_norm_args& a = *args;
+  mq_status st = check_norm(a);
+  if (st != MQ_OK) return st;
+  const int64_t blocks = (a.width + 127) / 128;
+  if (!a.h_out || !aligned(a.h_out, 16) || a.h_stride < 128 * blocks || a.h_stride % 16 != 0) return MQ_ERR_INVALID_ARG;
+  if (!scales_dev || scales_stride < blocks) return MQ_ERR_INVALID_ARG;
+  st = check_norm_rest(a);
+  if (st != MQ_OK) return st;
+  return from_hip(mq::launch_norm_residual_q8(a, static_cast<uint8_t*>(scales_dev), scales_stride,
+                                              static_cast<hipStream_t>(hip_stream)));
 }

@@ -79,5 +79,6 @@ hipError_t launch_kv_attention(const KvView& kv, int dim, int format, const Batc
                                float scale, RowsOut out, void* ws, const AttnPlan& plan, hipStream_t s);
 
 hipError_t launch_norm_residual(const mq_norm_args& a, hipStream_t s);
+hipError_t launch_norm_residual_q8(const mq_norm_args& a, uint8_t* scales, int64_t scales_stride, hipStream_t s);
 
 }  // namespace mq

@@ -1,5 +1,5 @@
 // Norms before and after a block with its gate and residual
-// (include/mosaicq_block.h, mq_norm_residual).
+// (include/mosaicq_block.h, mq_norm_residual and mq_norm_residual_q8).
 //
 //   r' = alpha r + beta g (y / rms(y)) (w_post + o),  h = (r' / rms(r')) (w_pre + o)
 //
@@ -11,9 +11,16 @@
 // rows of 8192, fp32 residual and a gate (470 MB): 87 us, 5.4 TB/s, the rate of
 // a large copy; 16 rows of 4096: 4.3 us. Rows past 32768 elements spill.
 #include "block_common.h"
+#include "q8.h"
 
 namespace mq {
 namespace {
+
+// Where 8-bit rows get their scales; h_out and h_stride are the codes' then.
+struct ScalesOut {
+  uint8_t* p;
+  int64_t stride;
+};
 
 template <int WAVES>
 __device__ __forceinline__ float sum_group(float v, float* lds) {
@@ -76,9 +83,11 @@ __device__ __forceinline__ void put8(float* p, int left, const float* v) {
 }
 
 // CH pieces of 8 elements a thread. Multiply-adds are written out, so that all
-// instances give the same bits.
-template <typename R, int THREADS, int CH>
-__global__ __launch_bounds__(THREADS) void k_norm(mq_norm_args a) {
+// instances give the same bits. Q8: h goes out as 8-bit rows, coded from its
+// fp32 values (one rounding); a block of 128 lies in 16 lanes that follow each
+// other, so its largest magnitude takes four lane exchanges and no LDS.
+template <typename R, int THREADS, int CH, bool Q8>
+__global__ __launch_bounds__(THREADS) void k_norm(mq_norm_args a, ScalesOut sc) {
   __shared__ float lds[2][THREADS / 64];
   const int64_t row = blockIdx.x;
   const int width = (int)a.width, tid = threadIdx.x;
@@ -141,13 +150,28 @@ __global__ __launch_bounds__(THREADS) void k_norm(mq_norm_args a) {
     take8(static_cast<const _Float16*>(a.w_pre) + d, left, w);
 #pragma unroll
     for (int i = 0; i < 8; ++i) w[i] = fp32(v[c][i] * scale * (w[i] + a.weight_offset));
-    put8(static_cast<_Float16*>(a.h_out) + row * a.h_stride + d, left, w);
+    if constexpr (Q8) {
+      uint32_t top = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (i >= left) w[i] = 0.0f;   // also where the row's scale is NaN
+        top = max(top, q8_magnitude(w[i]));
+      }
+      const uint32_t byte = q8_scale(q8_top16(top));
+      const int first = d & ~(kQ8Block - 1);
+      if (first < width) {
+        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.h_out) + row * a.h_stride + d) = q8_codes(w, byte);
+        if (d == first) sc.p[row * sc.stride + d / kQ8Block] = (uint8_t)byte;
+      }
+    } else {
+      put8(static_cast<_Float16*>(a.h_out) + row * a.h_stride + d, left, w);
+    }
   }
 }
 
 // A launch takes fewer than 2^32 threads: more rows than that run in pieces of 2^31.
-template <typename R, int THREADS, int CH>
-hipError_t go(const mq_norm_args& a, hipStream_t s) {
+template <typename R, bool Q8, int THREADS, int CH>
+hipError_t go(const mq_norm_args& a, const ScalesOut& sc, hipStream_t s) {
   constexpr int64_t step = (int64_t(1) << 31) / THREADS;
   for (int64_t t = 0; t < a.tokens; t += step) {
     mq_norm_args p = a;
@@ -156,28 +180,34 @@ hipError_t go(const mq_norm_args& a, hipStream_t s) {
     if (a.gate) p.gate = static_cast<const _Float16*>(a.gate) + t * a.gate_stride;
     p.r = static_cast<const R*>(a.r) + t * a.r_stride;
     if (a.y) p.r_out = static_cast<R*>(a.r_out) + t * a.r_out_stride;
-    if (a.w_pre) p.h_out = static_cast<_Float16*>(a.h_out) + t * a.h_stride;
-    k_norm<R, THREADS, CH><<<dim3((unsigned)p.tokens), dim3(THREADS), 0, s>>>(p);
+    if (a.w_pre) p.h_out = static_cast<uint8_t*>(a.h_out) + t * a.h_stride * (Q8 ? 1 : 2);
+    const ScalesOut q{Q8 ? sc.p + t * sc.stride : nullptr, sc.stride};
+    k_norm<R, THREADS, CH, Q8><<<dim3((unsigned)p.tokens), dim3(THREADS), 0, s>>>(p, q);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
 }
 
-template <typename R>
-hipError_t dispatch(const mq_norm_args& a, hipStream_t s) {
-  if (a.width <= 2048) return go<R, 256, 1>(a, s);
-  if (a.width <= 4096) return go<R, 512, 1>(a, s);
-  if (a.width <= 8192) return go<R, 1024, 1>(a, s);
-  if (a.width <= 16384) return go<R, 1024, 2>(a, s);
-  if (a.width <= 32768) return go<R, 1024, 4>(a, s);
-  return go<R, 1024, 8>(a, s);
+template <typename R, bool Q8>
+hipError_t dispatch(const mq_norm_args& a, const ScalesOut& sc, hipStream_t s) {
+  if (a.width <= 2048) return go<R, Q8, 256, 1>(a, sc, s);
+  if (a.width <= 4096) return go<R, Q8, 512, 1>(a, sc, s);
+  if (a.width <= 8192) return go<R, Q8, 1024, 1>(a, sc, s);
+  if (a.width <= 16384) return go<R, Q8, 1024, 2>(a, sc, s);
+  if (a.width <= 32768) return go<R, Q8, 1024, 4>(a, sc, s);
+  return go<R, Q8, 1024, 8>(a, sc, s);
 }
 
 }  // namespace
 
 hipError_t launch_norm_residual(const mq_norm_args& a, hipStream_t s) {
-  return a.residual_fp32 ? dispatch<float>(a, s) : dispatch<_Float16>(a, s);
+  return a.residual_fp32 ? dispatch<float, false>(a, {}, s) : dispatch<_Float16, false>(a, {}, s);
+}
+
+hipError_t launch_norm_residual_q8(const mq_norm_args& a, uint8_t* scales, int64_t scales_stride, hipStream_t s) {
+  const ScalesOut sc{scales, scales_stride};
+  return a.residual_fp32 ? dispatch<float, true>(a, sc, s) : dispatch<_Float16, true>(a, sc, s);
 }
 
 }  // namespace mq

@@ -3,7 +3,7 @@
  * linears of a decoder block (mosaicq.h) when it serves: rotary positions,
  * the append to a key/value cache held in 8 bits, the attention that reads
  * that cache, and the norms before and after a block with its gate and
- * residual. Library: libmosaicq_block.so, which stands beside libmosaicq.so
+ * residual, also with an output in 8 bits. Library: libmosaicq_block.so, which stands beside libmosaicq.so
  * and needs nothing of it (mq_status is shared).
  *
  * Conventions, as in mosaicq.h: pointers named *_dev (and every pointer in
@@ -236,6 +236,21 @@ typedef struct {
  * below width, misaligned elements, a scalar that is not finite),
  * MQ_ERR_UNSUPPORTED (width > 65536, tokens >= 2^31), MQ_ERR_DEVICE. */
 mq_status mq_norm_residual(const mq_norm_args* args, void* hip_stream);
+
+/*
+ * mq_norm_residual_q8 -- mq_norm_residual with h as 8-bit rows, for the linears
+ * that take them (mosaicq_head.h): r' is the same bits, and h, before it is
+ * rounded to fp16, is coded as mq_quantize8 codes (OCP e4m3 codes with a
+ * power-of-two scale for each block of 128 elements, rounded once).
+ *
+ *   args         as above with w_pre; h_out is the codes, [tokens, K8] bytes,
+ *                K8 = 128 ceil(width / 128), 16-byte aligned, rows h_stride bytes
+ *                apart (>= K8, a multiple of 16); bytes past width, up to K8, are 0
+ *   scales_dev   [tokens, K8 / 128] bytes, rows scales_stride bytes apart
+ *
+ * Errors as mq_norm_residual, and MQ_ERR_INVALID_ARG without w_pre.
+ */
+mq_status mq_norm_residual_q8(const mq_norm_args* args, void* scales_dev, int64_t scales_stride, void* hip_stream);
 
 #ifdef __cplusplus
 }
