@@ -35,31 +35,52 @@ constexpr int kGroup = 512, kGroupWaves = kGroup / 64;      // k_top, k_weigh, k
 constexpr int kPick = 256;                 // k_pick: what runs once costs each wave of a SIMD its issue slots
 constexpr int kRow = 512;                  // k_row
 constexpr int kMostSegs = 512;             // segments of a row
-constexpr int64_t kRowMost = 32768;        // tokens of a row that one workgroup takes,
+constexpr int64_t kRowMost = 16384;        // tokens of a row that one workgroup takes,
 constexpr int64_t kManyRows = 192, kManyMost = 512 * kMostSegs;      // and of each of many rows
 constexpr int64_t kRowsAtOnce = 1024;      // rows that share the workspace
 
-__device__ __forceinline__ void take8(const _Float16* p, int left, float* v) {
-  if (left >= 8) {
-    const half8_t h = load8(p);
+// Eight logits as they lie, asked for and not waited for; -Inf where the row has ended.
+template <typename T>
+struct Eight {
+  typedef T raw_t __attribute__((ext_vector_type(8)));
+  typedef T any_t __attribute__((ext_vector_type(8), aligned(sizeof(T))));
+  raw_t q;
+  __device__ __forceinline__ void ask(const T* p, int left) {
+    if (left >= 8) {
+      q = *reinterpret_cast<const any_t*>(p);
+    } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = (float)h[i];
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = i < left ? (float)p[i] : -__builtin_inff();
-  }
-}
-__device__ __forceinline__ void take8(const float* p, int left, float* v) {
-  if (left >= 8) {
-    const float4_t a = reinterpret_cast<const float4_any_t*>(p)[0], b = reinterpret_cast<const float4_any_t*>(p + 4)[0];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[i] = a[i];
-      v[i + 4] = b[i];
+      for (int i = 0; i < 8; ++i) q[i] = i < left ? p[i] : (T)-__builtin_inff();
     }
-  } else {
+  }
+  __device__ __forceinline__ void get(float* v) const {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = i < left ? p[i] : -__builtin_inff();
+    for (int i = 0; i < 8; ++i) v[i] = (float)q[i];
+  }
+};
+
+// f(v, at, s) of the wave's pieces s = first, first + step .. < end of 512 tokens each, 8 a lane. Four are asked for before
+// the first is used: a wave that waits for each by itself spends its time on that (256 rows of 50257: 24 us, so 17).
+template <typename T, typename F>
+__device__ __forceinline__ void each_piece(const T* row, int vocab, int first, int end, int step, F&& f) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll 1
+  for (int s0 = first; s0 < end; s0 += 4 * step) {
+    Eight<T> q[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int s = s0 + u * step;
+      if (s < end) q[u].ask(row + 512 * s + 8 * lane, vocab - 512 * s - 8 * lane);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int s = s0 + u * step;
+      if (s < end) {
+        float v[8];
+        q[u].get(v);
+        f(v, 512 * s + 8 * lane, s);
+      }
+    }
   }
 }
 
@@ -75,32 +96,38 @@ __device__ __forceinline__ float logit_of(uint32_t key) {
 __device__ __forceinline__ u64 place_of(float l, int token) { return ((u64)~key_of(l) << 32) | (uint32_t)token; }
 __device__ __forceinline__ float logit_at(u64 place) { return logit_of(~(uint32_t)(place >> 32)); }
 
-// rint(2^40 exp((l - top) / t)). With y = 32 (l - top) / (t ln 2) = n + r, n whole, the power is 2^(n / 32) 2^(r / 32): the
-// first from a table of 32 and an exponent, the second the series of exp to the sixth power (the rest is under 2^-57, |r|
-// <= 1/2). Adding 2^52 leaves the whole number in the low bits. No branch, so that a thread's eight run side by side: each
-// by itself is a chain of 15 dependent fp64 steps. What lies beyond 2^-43 of the largest counts as that far, and gives 0.
+// a b + c, c from scalar registers: a constant there needs no copy for each use.
+__device__ __forceinline__ double fma_c(double a, double b, double c) {
+  double d;
+  asm("v_fma_f64 %0, %1, %2, %3" : "=v"(d) : "v"(a), "v"(b), "s"(c));
+  return d;
+}
+
+// rint(2^40 exp((l - top) / t)). With y = 256 (l - top) / (t ln 2) = n + r, n whole, the power is 2^(n / 256) 2^(r / 256):
+// the first from a table of 256 and an exponent, the second the series of exp to the fourth power (the rest is under 2^-54,
+// |r| <= 1/2). Adding 2^52 leaves the whole number in the low bits. No branch, so that a thread's eight run side by side:
+// each by itself is a chain of 13 dependent fp64 steps. What lies beyond 2^-43 of the largest counts as that far, and gives
+// 0. (With a table of 32 and the sixth power, the constants copied: 64 x 131072 51 us, so 45.)
+constexpr int kTable = 256;
 struct Weigher {
   double top, scale;
-  const double* table;     // 2^(i / 32), in LDS
+  const double* table;     // 2^(i / 256), in LDS
   __device__ __forceinline__ u64 operator()(float l) const {
-    const double y = fmax(((double)l - top) * scale, -1376.0);
+    const double y = fmax(((double)l - top) * scale, -43.0 * kTable);
     const double n = rint(y), r = y - n;
-    constexpr double c = 0.6931471805599453 / 32.0;
-    double p = c * c * c * c * c * c / 720.0;
-    p = fma(p, r, c * c * c * c * c / 120.0);
-    p = fma(p, r, c * c * c * c / 24.0);
-    p = fma(p, r, c * c * c / 6.0);
-    p = fma(p, r, c * c / 2.0);
-    p = fma(p, r, c);
+    constexpr double c = 0.6931471805599453 / kTable;
+    double p = fma_c(r, c * c * c * c / 24.0, c * c * c / 6.0);
+    p = fma_c(p, r, c * c / 2.0);
+    p = fma_c(p, r, c);
     p = fma(p, r, 1.0);
     const int k = (int)n;
-    const double w = ldexp(p * table[k & 31], (k >> 5) + 40) + 4503599627370496.0;
+    const double w = ldexp(p * table[k & (kTable - 1)], (k >> 8) + 40) + 4503599627370496.0;
     return __builtin_bit_cast(u64, w) & 0xFFFFFFFFFFFFFull;
   }
 };
 // Fills the table; the caller's next barrier publishes it.
 __device__ __forceinline__ void fill_table(double* table) {
-  if (threadIdx.x < 32) table[threadIdx.x] = exp2((double)threadIdx.x / 32.0);
+  if (threadIdx.x < kTable) table[threadIdx.x] = exp2((double)threadIdx.x / kTable);
 }
 
 // floor(f total), f in 0 .. 1 taken to 31 bits, at most `most` steps of 2^-31; total < 2^62.
@@ -219,10 +246,14 @@ struct Row {
 };
 __device__ __forceinline__ Row row_of(const mq_sample_args& a, int64_t r, const Range& g, const double* table) {
   Row x;
-  const float t = a.temperature ? a.temperature[r] : 1.0f, min_p = a.min_p ? a.min_p[r] : 0.0f;
-  x.top_k = a.top_k ? a.top_k[r] : 0;
-  x.top_p = a.top_p ? a.top_p[r] : 1.0f;
-  x.u = a.u[r];
+  // a setting that is not given reads u in its place, so that all five are on their way at once
+  const float t_ = unwritten((a.temperature ? a.temperature : a.u) + r), top_p_ = unwritten((a.top_p ? a.top_p : a.u) + r),
+              min_p_ = unwritten((a.min_p ? a.min_p : a.u) + r);
+  const int top_k_ = unwritten((a.top_k ? a.top_k : reinterpret_cast<const int32_t*>(a.u)) + r);
+  x.u = unwritten(a.u + r);
+  const float t = a.temperature ? t_ : 1.0f, min_p = a.min_p ? min_p_ : 0.0f;
+  x.top_k = a.top_k ? top_k_ : 0;
+  x.top_p = a.top_p ? top_p_ : 1.0f;
   x.bad = g.bad || !(g.top > -__builtin_inff()) || !(t >= 0.0f) || !(t < __builtin_inff());
   x.greedy = t == 0.0f;
   if (!x.greedy) x.bad |= x.top_p != x.top_p || min_p != min_p || x.u != x.u;
@@ -232,7 +263,7 @@ __device__ __forceinline__ Row row_of(const mq_sample_args& a, int64_t r, const 
   x.least = min_p > 0.0f ? (u64)ceil(fmin((double)min_p, 1.0) * kOne) : 0ull;
   x.top = g.top;
   x.step = ((float)kBins - 0.01f) / fmaxf(fminf(0.5f * kReach * t, 0.5f * g.top - 0.5f * g.low), 1e-30f);
-  x.weight = {(double)g.top, 32.0 / ((double)t * 0.6931471805599453), table};
+  x.weight = {(double)g.top, kTable / ((double)t * 0.6931471805599453), table};
   return x;
 }
 // The step of a logit: it never falls as the logit does, so a prefix of the steps is a prefix of the order. kBins for one
@@ -390,17 +421,47 @@ struct Lds {
   uint32_t ties[kMostSegs];
   u64 scan[kRow / 64];
   Range range[kRow / 64];
-  double table[32];
+  double table[kTable];
   Limits limits;
   u64 a, b;
   uint32_t fill;
   int i, n1;
 };
 
-// The places p[0 .. n2) in order; n2 a power of two. A wave's 64 pairs are 128 places that follow each other while partners
-// are up to 64 apart: those steps need the wave alone, and no barrier.
+// The n places in order. Few: each thread counts the places before its own and puts them there: n steps that do not wait for
+// each other, as the 45 of the network for 512 do (64 rows, 320 places in most: k_pick 17 us by the network).
+constexpr int kCounted = 512;
 template <int THREADS>
-__device__ __forceinline__ void sort_places(u64* p, int n2) {
+__device__ __forceinline__ void sort_places(u64* p, int n) {
+  constexpr int kPer = kCounted / THREADS;
+  const int tid = threadIdx.x;
+  if (n <= kCounted) {
+    u64 mine[kPer];
+    int at[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      mine[i] = THREADS * i + tid < n ? p[THREADS * i + tid] : ~0ull;
+      at[i] = 0;
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      if (THREADS * i + (tid & ~63) < n) {
+#pragma unroll 8
+        for (int e = 0; e < n; ++e) at[i] += p[e] < mine[i];
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (THREADS * i + tid < n) p[at[i]] = mine[i];
+    __syncthreads();
+    return;
+  }
+  // Pairs in a network: a wave's 64 pairs are 128 places that follow each other while partners are up to 64 apart, and
+  // those steps need the wave alone, and no barrier.
+  int n2 = 2 * kCounted;
+  while (n2 < n) n2 <<= 1;
+  for (int e = n + tid; e < n2; e += THREADS) p[e] = ~0ull;
   bool alone = false;        // whether the last step was the wave's own
 #pragma unroll 1
   for (int k = 2; k <= n2; k <<= 1) {
@@ -414,7 +475,7 @@ __device__ __forceinline__ void sort_places(u64* p, int n2) {
       }
       alone = j <= 64;
 #pragma unroll 1
-      for (int e = threadIdx.x; e < n2 / 2; e += THREADS) {
+      for (int e = tid; e < n2 / 2; e += THREADS) {
         const int i = ((e & ~(j - 1)) << 1) | (e & (j - 1)), o = i | j;
         const u64 a = p[i], b = p[o];
         if ((a > b) == ((i & k) == 0)) {
@@ -433,14 +494,11 @@ __device__ __forceinline__ void sort_places(u64* p, int n2) {
 template <int THREADS>
 __device__ __forceinline__ u64 end_of_list(Lds& s, const Row& x, const Limits& z, int n, int span) {
   const int tid = threadIdx.x;
-  int n2 = 64;
-  while (n2 < n) n2 <<= 1;
-  for (int e = n + tid; e < n2; e += THREADS) s.place[e] = ~0ull;
   if (tid == 0) {
     s.i = 0;
     s.n1 = 0;
   }
-  sort_places<THREADS>(s.place, n2);
+  sort_places<THREADS>(s.place, n);
   // The first n1 are the steps from p0 to p1; the others, behind a gap, step k. Sums of the weights before each.
   const bool gap = z.k > z.p1 && z.k < kBins;
   u64 sum = 0;
@@ -544,8 +602,10 @@ __device__ __forceinline__ void draw_token(Lds& s, const mq_sample_args& a, int6
     const int at = at0 + 8 * (int)threadIdx.x;
     u64 y[8] = {}, m = 0;
     if (at < stop) {
+      Eight<T> q;
       float v[8];
-      take8(row + at, vocab - at, v);
+      q.ask(row + at, vocab - at);
+      q.get(v);
 #pragma unroll
       for (int i = 0; i < 8; ++i) m += y[i] = kept(x, end, v[i], at + i);
     }
@@ -556,14 +616,10 @@ __device__ __forceinline__ void draw_token(Lds& s, const mq_sample_args& a, int6
   }
 }
 
+// The pieces of a segment.
 template <typename T, typename F>
-__device__ __forceinline__ void each8(const T* row, int vocab, int seg, int span, F&& f) {
-  const int end = min(vocab, (seg + 1) * span);
-  for (int at = seg * span + 8 * (int)(threadIdx.x & 63); at < end; at += 512) {
-    float v[8];
-    take8(row + at, vocab - at, v);
-    f(v, at);
-  }
+__device__ __forceinline__ void each_of_segment(const T* row, int vocab, int seg, int span, F&& f) {
+  each_piece(row, vocab, seg * (span / 512), min((vocab + 511) / 512, (seg + 1) * (span / 512)), 1, f);
 }
 
 // The slow way: the limits by a search over the digits of the key, each a pass over the row. Needs no list, so it takes
@@ -588,8 +644,10 @@ __device__ __forceinline__ Cut find_cut(Lds& sh, const Row& x, const T* row, int
     }
     __syncthreads();
     for (int at = 512 * wave + 8 * lane; at < vocab; at += 8 * THREADS) {
+      Eight<T> q;
       float v[8];
-      take8(row + at, vocab - at, v);
+      q.ask(row + at, vocab - at);
+      q.get(v);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const uint32_t k = key_of(v[i]);
@@ -658,7 +716,7 @@ __device__ __forceinline__ void pick_by_digits(const mq_sample_args& a, int64_t 
   // the segments' sums above the cut, and their ties
   for (int s = wave; s < segs; s += THREADS / 64) {
     u64 m = 0, n = 0;
-    each8(row, vocab, s, span, [&](const float* v, int at) {
+    each_of_segment(row, vocab, s, span, [&](const float* v, int at, int) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const uint32_t k = key_of(v[i]);
@@ -706,7 +764,9 @@ __device__ __forceinline__ void pick_by_digits(const mq_sample_args& a, int64_t 
     float v[8] = {};
     u64 y[8] = {}, m = 0, k = 0;
     if (at < stop) {
-      take8(row + at, vocab - at, v);
+      Eight<T> q;
+      q.ask(row + at, vocab - at);
+      q.get(v);
 #pragma unroll
       for (int i = 0; i < 8; ++i) k += key_of(v[i]) == cut.key && at + i < vocab;
     }
@@ -746,16 +806,7 @@ __global__ __launch_bounds__(kRow) void k_row(mq_sample_args a, int segs) {
     s.count[b] = 0;
   }
   if (tid == 0) s.fill = 0;
-  // f of each 512 tokens that the wave has
-  auto each = [&](auto&& f) {
-#pragma unroll 1
-    for (int seg = wave; seg < segs; seg += kRow / 64) {
-      const int at = 512 * seg + 8 * lane;
-      float v[8];
-      take8(row + at, vocab - at, v);
-      f(v, at, seg);
-    }
-  };
+  auto each = [&](auto&& f) { each_piece(row, vocab, wave, segs, kRow / 64, f); };
   Range g = no_range();
   each([&](const float* v, int at, int) { look8(g, v, at); });
   g = join64(g);
@@ -815,8 +866,8 @@ __global__ __launch_bounds__(kGroup) void k_top(mq_sample_args a, Work w, int li
     if (s == 0 && tid == 0) w.fill[r] = 0;
   }
   Range g = no_range();
-  each8(static_cast<const T*>(a.logits) + r * a.stride, (int)a.vocab, kGroupWaves * s + (tid >> 6), w.span,
-        [&](const float* v, int at) { look8(g, v, at); });
+  each_of_segment(static_cast<const T*>(a.logits) + r * a.stride, (int)a.vocab, kGroupWaves * s + (tid >> 6), w.span,
+        [&](const float* v, int at, int) { look8(g, v, at); });
   g = join64(g);
   if ((tid & 63) == 0) lds[tid >> 6] = g;
   __syncthreads();
@@ -828,7 +879,7 @@ template <typename T>
 __global__ __launch_bounds__(kGroup) void k_weigh(mq_sample_args a, Work w) {
   __shared__ u64 mass[kBins];
   __shared__ uint32_t count[kBins];
-  __shared__ double table[32];
+  __shared__ double table[kTable];
   const int64_t r = blockIdx.y;
   const int tid = threadIdx.x, seg = kGroupWaves * blockIdx.x + (tid >> 6);
   fill_table(table);
@@ -842,12 +893,12 @@ __global__ __launch_bounds__(kGroup) void k_weigh(mq_sample_args a, Work w) {
   const T* row = static_cast<const T*>(a.logits) + r * a.stride;
   if (!x.has_k && !x.has_p) {
     u64 m = 0;
-    each8(row, (int)a.vocab, seg, w.span, [&](const float* v, int) { m += sum8(x, v); });
+    each_of_segment(row, (int)a.vocab, seg, w.span, [&](const float* v, int, int) { m += sum8(x, v); });
     m = sum64(m);
     if ((tid & 63) == 0) w.seg[r * kGroupWaves * w.splits + seg] = m;
     return;
   }
-  each8(row, (int)a.vocab, seg, w.span, [&](const float* v, int) { add8(x, v, mass, count); });
+  each_of_segment(row, (int)a.vocab, seg, w.span, [&](const float* v, int, int) { add8(x, v, mass, count); });
   __syncthreads();
   for (int b = tid; b < kBins; b += kGroup) {
     if (mass[b]) atomicAdd(&w.mass[r * kBins + b], mass[b]);
@@ -859,7 +910,7 @@ template <typename T>
 __global__ __launch_bounds__(kGroup) void k_gather(mq_sample_args a, Work w) {
   __shared__ u64 lds[kGroupWaves], list[kList];
   __shared__ Limits lds_limits;
-  __shared__ double table[32];
+  __shared__ double table[kTable];
   __shared__ uint32_t fill, base;
   const int64_t r = blockIdx.y;
   const int tid = threadIdx.x, seg = kGroupWaves * blockIdx.x + (tid >> 6);
@@ -870,8 +921,8 @@ __global__ __launch_bounds__(kGroup) void k_gather(mq_sample_args a, Work w) {
   const Limits z = find_limits<kGroup>(x, w.mass + r * kBins, w.count + r * kBins, lds, &lds_limits);
   if (blockIdx.x == 0 && tid == 0) w.limits[r] = z;
   u64 m = 0;
-  each8(static_cast<const T*>(a.logits) + r * a.stride, (int)a.vocab, seg, w.span,
-        [&](const float* v, int at) { m += gather8(x, z, v, at, &fill, list); });
+  each_of_segment(static_cast<const T*>(a.logits) + r * a.stride, (int)a.vocab, seg, w.span,
+        [&](const float* v, int at, int) { m += gather8(x, z, v, at, &fill, list); });
   m = sum64(m);
   if ((tid & 63) == 0) w.seg[r * kGroupWaves * w.splits + seg] = m;
   // the workgroup's list joins the row's; their order there is any: k_pick sorts them
