@@ -139,9 +139,14 @@ hipError_t go_stream(const Rows8& x, int64_t M, const W8& w, _Float16* y, int64_
 // A workgroup of 4 waves makes 64 RB weight rows x 128 tokens; a wave its own
 // 16 RB rows with all the tokens. The weights lie in the instruction's order,
 // so they go from L2 straight to registers; the tokens' codes go to LDS, where
-// the waves share them, by direct copies one block of 128 columns ahead.
+// the waves share them, by direct copies three blocks of 128 columns ahead (two
+// workgroups a CU). Steps are taken by fours, which share the words of scales;
+// what lies past K in the last four is zero in LDS and adds nothing. Nothing in
+// a step is under a condition: a load there would be waited for where the
+// branches meet.
 constexpr int kTb = 8;           // blocks of 16 tokens a workgroup
 constexpr int kStage = kTb * kTile;
+constexpr int kTiledLds = 4 * kStage + 2 * (256 + 256) * 4;      // codes; scale words of the tokens and the weight rows
 
 // The codes of 16 tokens x 128 columns in LDS are filled by two copies of 1 KiB, in lane order. Copy u, lane l brings row
 // l / 4, chunk 4 u + (l % 4 ^ row / 2 % 4) of its 8 chunks of 16 bytes: quads read runs of 64 bytes, and the 8 lanes that
@@ -152,49 +157,81 @@ __device__ __forceinline__ uint32_t stage_pos(int lane) {
   return 16u * (uint32_t)(4 * n + (g ^ ((n >> 1) & 3)));
 }
 
+// A barrier for LDS alone: loads stay on their way.
+__device__ __forceinline__ void lds_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+
 template <int RB>
 __global__ __launch_bounds__(256, 2) void k_tiled8(Rows8 x, int M, W8 w, _Float16* y, int64_t ys, float* part, int NT,
                                                    int T, int per) {
-  __shared__ __attribute__((aligned(16))) uint8_t stage[2][kStage];
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+  constexpr int kAhead = RB == 4 ? 1 : 3;      // steps that the weights are asked for ahead: what the registers hold
+  constexpr int kSets = kAhead + 1;
+  constexpr int kCopies = 2 * (kTb / 4);       // of a wave in a step
+  uint32_t* const scale_lds = reinterpret_cast<uint32_t*>(lds + 4 * kStage);
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int r = lane & 15, g = lane >> 4;
   const int tile = xcd_tile(blockIdx.x, T), MT = T / NT;
   const int nt = tile / MT, mt = tile - nt * MT;
   const int rb0 = (nt * 4 + wave) * RB, m0 = 16 * kTb * mt;
-  const int kt0 = blockIdx.y * per, kt1 = min(w.Kt, kt0 + per);
+  const int kt0 = blockIdx.y * per, kt1 = min(w.Kt, kt0 + per), q1 = (kt1 + 3) >> 2;
 
   // the workgroup's token rows; reads past them give zero
   const int rows = min(16 * kTb, M - m0);
+  const uint32_t range = (uint32_t)rows * (uint32_t)x.stride;
   const __amdgpu_buffer_rsrc_t xr = __builtin_amdgcn_make_buffer_rsrc(
-      const_cast<uint8_t*>(x.codes + (int64_t)m0 * x.stride), 0, (int)(rows * x.stride), kBufferRaw);
+      const_cast<uint8_t*>(x.codes + (int64_t)m0 * x.stride), 0, (int)range, kBufferRaw);
   const uint32_t xl = (uint32_t)(lane >> 2) * (uint32_t)x.stride + 16u * stage_chunk(lane);
-  auto copy = [&](uint8_t* to, int kt) {
+  auto copy = [&](int stage, int kt) {
+    const uint32_t at = kt < kt1 ? (uint32_t)kt * kQ8Block : 0x40000000u;      // past the split: zero
 #pragma unroll
     for (int i = 0; i < kTb / 4; ++i)
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const int tb = (kTb / 4) * wave + i;
         __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            xr, (__attribute__((address_space(3))) void*)(to + tb * kTile + 1024 * u), 16,
-            xl + (uint32_t)(16 * tb) * (uint32_t)x.stride + (uint32_t)(kt * kQ8Block + 64 * u), 0, 0, 0);
+            xr, (__attribute__((address_space(3))) void*)(lds + stage * kStage + tb * kTile + 1024 * u), 16,
+            xl + (uint32_t)(16 * tb) * (uint32_t)x.stride + at + 64 * u, 0, 0, 0);
       }
   };
-  const uint8_t* wc[RB];
-  const uint8_t* wsc[RB];
-#pragma unroll
-  for (int i = 0; i < RB; ++i) {
-    const int64_t rb = min(rb0 + i, w.Nb - 1);
-    wc[i] = w.codes + kTile * rb * w.Kt;
-    wsc[i] = w.scales + 64 * rb * w.Kq;
-  }
-  auto weights = [&](i32x8_t(&a)[RB], int kt) {
+  // the wave's weight rows: one offset a lane, the tile's in a scalar register (rows past the last block repeat it)
+  const int rbw = min(rb0, w.Nb - 1);
+  const __amdgpu_buffer_rsrc_t wr = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<uint8_t*>(w.codes + (int64_t)kTile * rbw * w.Kt), 0, 0x7FFFFFFF, kBufferRaw);
+  const int wl = 16 * lane;
+  i32x8_t a[kSets][RB];
+  auto weights = [&](int set, int kt) {
     kt = min(kt, w.Kt - 1);
 #pragma unroll
-    for (int i = 0; i < RB; ++i) a[i] = load_halves(wc[i] + (int64_t)kTile * kt + 16 * lane, 1024);
+    for (int i = 0; i < RB; ++i) {
+      const int at = (min(i, w.Nb - 1 - rbw) * w.Kt + kt) * kTile;
+      a[set][i] = join(__builtin_bit_cast(i32x4_t, __builtin_amdgcn_raw_buffer_load_b128(wr, wl, at, 0)),
+                       __builtin_bit_cast(i32x4_t, __builtin_amdgcn_raw_buffer_load_b128(wr, wl, at + 1024, 0)));
+    }
   };
-  const uint8_t* xs[kTb];
+  // The scales of four blocks: a thread asks for those of a token and of a weight row of the workgroup, and puts them into
+  // LDS as words two steps later.
+  const uint8_t* const xs = x.scales + (int64_t)min(m0 + (tid & 127), M - 1) * x.sstride;
+  const uint8_t* const ws = w.scales + 64 * (int64_t)min(nt * 4 * RB + (tid >> 4), w.Nb - 1) * w.Kq + 4 * (tid & 15);
+  uint32_t byte[4], word;
+  auto ask_scales = [&](int q) {
 #pragma unroll
-  for (int t = 0; t < kTb; ++t) xs[t] = x.scales + (int64_t)min(m0 + 16 * t + r, M - 1) * x.sstride;
+    for (int j = 0; j < 4; ++j) byte[j] = xs[min(4 * q + j, w.Kt - 1)];
+    word = *reinterpret_cast<const uint32_t*>(ws + 64 * min(q, w.Kq - 1));
+  };
+  auto put_scales = [&](int q) {
+    uint32_t* const to = scale_lds + (q & 1) * 512;      // tokens come twice: a branch here would part the step
+    to[tid] = byte[0] | (byte[1] << 8) | (byte[2] << 16) | (byte[3] << 24);
+    to[256 + tid] = word;
+  };
 
   float4_t acc[RB][kTb];
 #pragma unroll
@@ -202,39 +239,47 @@ __global__ __launch_bounds__(256, 2) void k_tiled8(Rows8 x, int M, W8 w, _Float1
 #pragma unroll
     for (int t = 0; t < kTb; ++t) acc[i][t] = float4_t{0.f, 0.f, 0.f, 0.f};
 
-  i32x8_t a0[RB], a1[RB];
-  copy(stage[0], kt0);
-  weights(a0, kt0);
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // the copies into LDS
-  __syncthreads();
+  const int q0 = kt0 >> 2;
+  ask_scales(q0);
+#pragma unroll
+  for (int j = 0; j < 3; ++j) copy(j, kt0 + j);
+#pragma unroll
+  for (int j = 0; j < kAhead; ++j) weights(j, kt0 + j);
+  put_scales(q0);
+  wait_loads<0>();
+  lds_barrier();
   const uint32_t pos = stage_pos(lane);
-  for (int q = kt0 >> 2; 4 * q < kt1; ++q) {
-    int sw[RB], sx[kTb];
+  for (int q = q0; q < q1; ++q) {
+    const uint32_t* const scale = scale_lds + (q & 1) * 512;
+    int sx[kTb], sw[RB];
 #pragma unroll
-    for (int i = 0; i < RB; ++i) sw[i] = *reinterpret_cast<const int*>(wsc[i] + 64 * q + 4 * r);
+    for (int t = 0; t < kTb; ++t) sx[t] = (int)scale[16 * t + r];
 #pragma unroll
-    for (int t = 0; t < kTb; ++t) sx[t] = row_scales(xs[t], q, w.Kt);
+    for (int i = 0; i < RB; ++i) sw[i] = (int)scale[256 + 16 * (wave * RB + i) + r];
+    ask_scales(q + 1);
     four([&](auto j) {
       const int kt = 4 * q + j;
-      if (kt < kt1) {
-        uint8_t* const cur = stage[j & 1];
-        i32x8_t(&a)[RB] = (j & 1) ? a1 : a0;
-        i32x8_t(&an)[RB] = (j & 1) ? a0 : a1;
-        if (kt + 1 < kt1) {
-          copy(stage[(j & 1) ^ 1], kt + 1);
-          weights(an, kt + 1);
-        }
+      copy((j + 3) & 3, kt + 3);
+      weights((j + kAhead) % kSets, kt + kAhead);
+      __builtin_amdgcn_sched_barrier(0);        // the loads go out first,
+      const uint8_t* const cur = lds + j * kStage + pos;
+      i32x8_t b[2];
+      b[0] = load_halves(cur, 1024);
 #pragma unroll
-        for (int t = 0; t < kTb; ++t) {
-          const i32x8_t b = load_halves(cur + t * kTile + pos, 1024);
+      for (int t = 0; t < kTb; ++t) {
+        if (t + 1 < kTb) b[(t + 1) & 1] = load_halves(cur + (t + 1) * kTile, 1024);
 #pragma unroll
-          for (int i = 0; i < RB; ++i) acc[i][t] = mfma8<j>(a[i], b, acc[i][t], sw[i], sx[t]);
-        }
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-        __syncthreads();
+        for (int i = 0; i < RB; ++i) acc[i][t] = mfma8<j>(a[j % kSets][i], b[t & 1], acc[i][t], sw[i], sx[t]);
+        asm volatile("" ::: "memory");          // and an operand from LDS just before the products with the one before it
+        __builtin_amdgcn_sched_barrier(0);
       }
+      if constexpr (j == 2) put_scales(q + 1);
+      // the copies for the next step have arrived when no more is on its way than the two steps after them asked for
+      wait_loads<2 * (kCopies + 2 * RB)>();
+      lds_barrier();
     }, std::make_integer_sequence<int, 4>{});
   }
+  wait_loads<0>();      // no copy outlives the workgroup's LDS
   float* const slice = part ? part + (int64_t)blockIdx.y * M * w.N : nullptr;
 #pragma unroll
   for (int i = 0; i < RB; ++i) {
@@ -272,9 +317,12 @@ template <int RB>
 hipError_t go_tiled(const Rows8& x, int64_t M, const W8& w, _Float16* y, int64_t ys, float* part,
                     const Linear8Plan& p, hipStream_t s) {
   const int NT = (w.Nb + 4 * RB - 1) / (4 * RB), MT = (int)((M + 16 * kTb - 1) / (16 * kTb));
-  k_tiled8<RB><<<dim3((unsigned)(NT * MT), (unsigned)p.splits), dim3(256), 0, s>>>(x, (int)M, w, y, ys, part, NT, NT * MT,
-                                                                                   p.per);
-  hipError_t e = hipGetLastError();
+  hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_tiled8<RB>),
+                                     hipFuncAttributeMaxDynamicSharedMemorySize, kTiledLds);
+  if (e != hipSuccess) return e;
+  k_tiled8<RB><<<dim3((unsigned)(NT * MT), (unsigned)p.splits), dim3(256), kTiledLds, s>>>(x, (int)M, w, y, ys, part, NT,
+                                                                                           NT * MT, p.per);
+  e = hipGetLastError();
   if (e == hipSuccess && part) {
     const int64_t groups = (M * w.N + 255) / 256;
     k_join8<<<dim3((unsigned)(groups < 8192 ? groups : 8192)), dim3(256), 0, s>>>(part, p.splits, M, w.N, y, ys);
