@@ -11,8 +11,8 @@ namespace {
 constexpr int64_t k31 = int64_t(1) << 31;
 constexpr int64_t kMostK = int64_t(1) << 20;
 constexpr int64_t kMostRows = int64_t(1) << 24;
-// The tiled kernel addresses a workgroup's 128 token rows by 32-bit offsets.
-constexpr int64_t kMostStride = int64_t(1) << 23;
+// The tiled kernel addresses a workgroup's 256 token rows by offsets under 2^30.
+constexpr int64_t kMostStride = int64_t(1) << 22;
 
 mq_status from_hip(hipError_t e) {
   if (e == hipSuccess) return MQ_OK;
@@ -111,7 +111,7 @@ MQ_API mq_status mq_linear8(const void* codes_dev, int64_t codes_stride, const v
   st = linear_plan(M, w, &plan);
   if (st != MQ_OK) return st;
   if (bad_rows8(codes_dev, codes_stride, scales_dev, scales_stride, w->K)) return MQ_ERR_INVALID_ARG;
-  if (codes_stride > kMostStride) return MQ_ERR_UNSUPPORTED;
+  if (codes_stride > kMostStride || scales_stride > kMostStride) return MQ_ERR_UNSUPPORTED;
   if (!Y_dev_fp16 || !aligned(Y_dev_fp16, 2) || y_stride < w->N) return MQ_ERR_INVALID_ARG;
   if (plan.bytes > 0 && (!workspace_dev || !aligned(workspace_dev, 16) || workspace_bytes < plan.bytes))
     return MQ_ERR_INVALID_ARG;

@@ -34,6 +34,7 @@ struct Linear8Plan {
   int nt;              // blocks of 16 tokens of the kernel that streams the weights; 0: the tiled kernel
   int r;               // its blocks of 16 weight rows a workgroup, or of the tiled kernel a wave
   int waves;           // its waves a workgroup
+  int tb;              // blocks of 16 tokens of the tiled kernel
   int splits;          // of the tiled kernel along K
   int per;             // blocks of 128 columns a split, a multiple of 4
   int64_t groups;      // workgroups in all, of 256 threads

@@ -43,10 +43,11 @@ __device__ __forceinline__ int row_scales(const uint8_t* row, int q, int Kt) {
   return (int)v;
 }
 
+// Four outputs that follow each other, of which `left` exist: one store, which memory takes at any address.
 __device__ __forceinline__ void put4(_Float16* y, float4_t v, int64_t left) {
-  typedef _Float16 half4_t __attribute__((ext_vector_type(4)));
-  if (left >= 4 && (reinterpret_cast<uintptr_t>(y) & 7) == 0) {
-    *reinterpret_cast<half4_t*>(y) = (half4_t){(_Float16)v[0], (_Float16)v[1], (_Float16)v[2], (_Float16)v[3]};
+  typedef _Float16 half4_any_t __attribute__((ext_vector_type(4), aligned(2)));
+  if (left >= 4) {
+    *reinterpret_cast<half4_any_t*>(y) = (half4_any_t){(_Float16)v[0], (_Float16)v[1], (_Float16)v[2], (_Float16)v[3]};
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -136,71 +137,68 @@ hipError_t go_stream(const Rows8& x, int64_t M, const W8& w, _Float16* y, int64_
 }
 
 // ----------------------------------------------------------- many tokens
-// A workgroup of 4 waves makes 64 RB weight rows x 128 tokens; a wave its own
+// A workgroup of 4 waves makes 64 RB weight rows x 16 TB tokens; a wave its own
 // 16 RB rows with all the tokens. The weights lie in the instruction's order,
 // so they go from L2 straight to registers; the tokens' codes go to LDS, where
-// the waves share them, by direct copies three blocks of 128 columns ahead (two
-// workgroups a CU). Steps are taken by fours, which share the words of scales;
+// the waves share them, by direct copies three blocks of 128 columns ahead. Steps are taken by fours, which share the words of scales;
 // what lies past K in the last four is zero in LDS and adds nothing. Nothing in
 // a step is under a condition: a load there would be waited for where the
 // branches meet.
-constexpr int kTb = 8;           // blocks of 16 tokens a workgroup
-constexpr int kStage = kTb * kTile;
-constexpr int kTiledLds = 4 * kStage + 2 * (256 + 256) * 4;      // codes; scale words of the tokens and the weight rows
+// codes; scales of the tokens, 16 blocks of each, and of the weight rows, 4 of each; each twice
+constexpr int tiled_lds(int rb, int tokens) { return 4 * tokens * kQ8Block + 2 * (16 * tokens + 4 * 64 * rb); }
 
 // The codes of 16 tokens x 128 columns in LDS are filled by two copies of 1 KiB, in lane order. Copy u, lane l brings row
-// l / 4, chunk 4 u + (l % 4 ^ row / 2 % 4) of its 8 chunks of 16 bytes: quads read runs of 64 bytes, and the 8 lanes that
-// LDS serves at once when the operand is read back (rows n .. n + 7, one chunk) find 8 different banks of 16 bytes.
-__device__ __forceinline__ uint32_t stage_chunk(int lane) { return (uint32_t)((lane & 3) ^ ((lane >> 3) & 3)); }
+// 8 u + l / 8, chunk l % 8 ^ l / 8 of its 8 chunks of 16 bytes: eight lanes read a row's whole line (quads with runs of 64
+// bytes ask for each line twice: X took twice the time of as many bytes of weights), and the 8 lanes that LDS serves at once
+// when the operand is read back (rows n .. n + 7, one chunk) find 8 different banks of 16 bytes.
+__device__ __forceinline__ uint32_t stage_from(int lane, uint32_t stride) {
+  return (uint32_t)(lane >> 3) * stride + 16u * (uint32_t)((lane & 7) ^ (lane >> 3));
+}
+// Where lane n + 16 g finds chunk g of row n; chunk 4 + g lies 64 bytes away from it, up or down.
 __device__ __forceinline__ uint32_t stage_pos(int lane) {
   const int n = lane & 15, g = lane >> 4;
-  return 16u * (uint32_t)(4 * n + (g ^ ((n >> 1) & 3)));
+  return 16u * (uint32_t)(8 * n + (g ^ (n & 7)));
 }
 
-// A barrier for LDS alone: loads stay on their way.
-__device__ __forceinline__ void lds_barrier() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
-  __builtin_amdgcn_s_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
-}
-
+// Waits until no more than N loads are on their way, and for the wave's own LDS accesses, then for the other waves. (A fence
+// would wait for every copy into LDS, also for those that the next steps need.)
 template <int N>
-__device__ __forceinline__ void wait_loads() {
-  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+__device__ __forceinline__ void wait_and_meet() {
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
 }
 
-template <int RB>
+template <int RB, int TB>
 __global__ __launch_bounds__(256, 2) void k_tiled8(Rows8 x, int M, W8 w, _Float16* y, int64_t ys, float* part, int NT,
                                                    int T, int per) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   constexpr int kAhead = RB == 4 ? 1 : 3;      // steps that the weights are asked for ahead: what the registers hold
   constexpr int kSets = kAhead + 1;
-  constexpr int kCopies = 2 * (kTb / 4);       // of a wave in a step
-  uint32_t* const scale_lds = reinterpret_cast<uint32_t*>(lds + 4 * kStage);
+  constexpr int kCopies = TB / 2;              // of a wave in a step
+  constexpr int kTokens = 16 * TB, kRows = 64 * RB, kStage = kTokens * kQ8Block;
+  uint4* const token_scales = reinterpret_cast<uint4*>(lds + 4 * kStage);
+  uint32_t* const row_scale_words = reinterpret_cast<uint32_t*>(lds + 4 * kStage + 2 * 16 * kTokens);
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int r = lane & 15, g = lane >> 4;
   const int tile = xcd_tile(blockIdx.x, T), MT = T / NT;
   const int nt = tile / MT, mt = tile - nt * MT;
-  const int rb0 = (nt * 4 + wave) * RB, m0 = 16 * kTb * mt;
+  const int rb0 = (nt * 4 + wave) * RB, m0 = kTokens * mt;
   const int kt0 = blockIdx.y * per, kt1 = min(w.Kt, kt0 + per), q1 = (kt1 + 3) >> 2;
 
   // the workgroup's token rows; reads past them give zero
-  const int rows = min(16 * kTb, M - m0);
+  const int rows = min(kTokens, M - m0);
   const uint32_t range = (uint32_t)rows * (uint32_t)x.stride;
   const __amdgpu_buffer_rsrc_t xr = __builtin_amdgcn_make_buffer_rsrc(
       const_cast<uint8_t*>(x.codes + (int64_t)m0 * x.stride), 0, (int)range, kBufferRaw);
-  const uint32_t xl = (uint32_t)(lane >> 2) * (uint32_t)x.stride + 16u * stage_chunk(lane);
+  const uint32_t xl = stage_from(lane, (uint32_t)x.stride);
   auto copy = [&](int stage, int kt) {
     const uint32_t at = kt < kt1 ? (uint32_t)kt * kQ8Block : 0x40000000u;      // past the split: zero
 #pragma unroll
-    for (int i = 0; i < kTb / 4; ++i)
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int tb = (kTb / 4) * wave + i;
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(
-            xr, (__attribute__((address_space(3))) void*)(lds + stage * kStage + tb * kTile + 1024 * u), 16,
-            xl + (uint32_t)(16 * tb) * (uint32_t)x.stride + at + 64 * u, 0, 0, 0);
-      }
+    for (int i = 0; i < kCopies; ++i) {
+      const int tb = (4 * i + wave) >> 1, u = wave & 1;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(
+          xr, (__attribute__((address_space(3))) void*)(lds + stage * kStage + tb * kTile + 1024 * u), 16,
+          xl + (uint32_t)(16 * tb + 8 * u) * (uint32_t)x.stride + at, 0, 0, 0);
+    }
   };
   // the wave's weight rows: one offset a lane, the tile's in a scalar register (rows past the last block repeat it)
   const int rbw = min(rb0, w.Nb - 1);
@@ -217,76 +215,109 @@ __global__ __launch_bounds__(256, 2) void k_tiled8(Rows8 x, int M, W8 w, _Float1
                        __builtin_bit_cast(i32x4_t, __builtin_amdgcn_raw_buffer_load_b128(wr, wl, at + 1024, 0)));
     }
   };
-  // The scales of four blocks: a thread asks for those of a token and of a weight row of the workgroup, and puts them into
-  // LDS as words two steps later.
-  const uint8_t* const xs = x.scales + (int64_t)min(m0 + (tid & 127), M - 1) * x.sstride;
-  const uint8_t* const ws = w.scales + 64 * (int64_t)min(nt * 4 * RB + (tid >> 4), w.Nb - 1) * w.Kq + 4 * (tid & 15);
-  uint32_t byte[4], word;
-  auto ask_scales = [&](int q) {
+  // The scales: a thread asks for 16 of a token's at a time, once in 16 steps (64 tokens are 64 lines: asked for by fours
+  // they were a sixth of all that came from L2), and for a word of a weight row's, four of them, once in 4; into LDS later.
+  // A token's 16 bytes are taken from where they lie, or, where that would pass the end of all scales, from some bytes before
+  // and shifted; bytes past the row count as 127 (their codes are zero, but a NaN there would not be).
+  const uint8_t* const xs = x.scales + (int64_t)m0 * x.sstride;
+  const int xs_own = min(tid % kTokens, M - 1 - m0) * (int)x.sstride;
+  const int xs_last = (int)min((int64_t)0x40000000, (M - 1 - m0) * x.sstride + w.Kt - 16);
+  const __amdgpu_buffer_rsrc_t wsr = __builtin_amdgcn_make_buffer_rsrc(
+      const_cast<uint8_t*>(w.scales + (int64_t)64 * min(nt * 4 * RB, w.Nb - 1) * w.Kq), 0, 0x7FFFFFFF, kBufferRaw);
+  const int ws_own = 64 * min(tid % kRows >> 4, w.Nb - 1 - min(nt * 4 * RB, w.Nb - 1)) * w.Kq + 4 * (tid & 15);
+  typedef unsigned __int128 u128;
+  u128 token_bytes;
+  int token_over;
+  uint32_t row_word;
+  auto ask_token_scales = [&](int q) {
+    const int at = xs_own + 4 * min(q, w.Kq - 1);
+    token_over = max(0, at - xs_last);
+    typedef u128 u128_any_t __attribute__((aligned(1)));
+    token_bytes = *reinterpret_cast<const u128_any_t*>(xs + (at - token_over));
+  };
+  auto put_token_scales = [&](int buffer, int q) {
+    const u128 v = token_bytes >> (8 * token_over);
+    const int have = w.Kt - 4 * min(q, w.Kq - 1);
+    uint32_t to[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) byte[j] = xs[min(4 * q + j, w.Kt - 1)];
-    word = *reinterpret_cast<const uint32_t*>(ws + 64 * min(q, w.Kq - 1));
+    for (int i = 0; i < 4; ++i) {
+      const int n = min(max(have - 4 * i, 0), 4);
+      const uint32_t own = n == 4 ? 0xFFFFFFFFu : (1u << (8 * n)) - 1;
+      to[i] = ((uint32_t)(v >> (32 * i)) & own) | (0x7F7F7F7Fu & ~own);
+    }
+    token_scales[buffer * kTokens + tid % kTokens] = make_uint4(to[0], to[1], to[2], to[3]);
   };
-  auto put_scales = [&](int q) {
-    uint32_t* const to = scale_lds + (q & 1) * 512;      // tokens come twice: a branch here would part the step
-    to[tid] = byte[0] | (byte[1] << 8) | (byte[2] << 16) | (byte[3] << 24);
-    to[256 + tid] = word;
-  };
+  auto ask_row_scales = [&](int q) { row_word = __builtin_amdgcn_raw_buffer_load_b32(wsr, ws_own, 64 * min(q, w.Kq - 1), 0); };
+  auto put_row_scales = [&](int q) { row_scale_words[(q & 1) * kRows + tid % kRows] = row_word; };
 
-  float4_t acc[RB][kTb];
+  float4_t acc[RB][TB];
 #pragma unroll
   for (int i = 0; i < RB; ++i)
 #pragma unroll
-    for (int t = 0; t < kTb; ++t) acc[i][t] = float4_t{0.f, 0.f, 0.f, 0.f};
+    for (int t = 0; t < TB; ++t) acc[i][t] = float4_t{0.f, 0.f, 0.f, 0.f};
 
   const int q0 = kt0 >> 2;
-  ask_scales(q0);
+  ask_token_scales(q0);
+  ask_row_scales(q0);
 #pragma unroll
   for (int j = 0; j < 3; ++j) copy(j, kt0 + j);
 #pragma unroll
   for (int j = 0; j < kAhead; ++j) weights(j, kt0 + j);
-  put_scales(q0);
-  wait_loads<0>();
-  lds_barrier();
-  const uint32_t pos = stage_pos(lane);
-  for (int q = q0; q < q1; ++q) {
-    const uint32_t* const scale = scale_lds + (q & 1) * 512;
-    int sx[kTb], sw[RB];
+  put_token_scales(0, q0);
+  put_row_scales(q0);
+  wait_and_meet<0>();
+  const uint32_t pos = stage_pos(lane), pos4 = pos ^ 64;
+  auto operand = [&](const uint8_t* p) {
+    return join(*reinterpret_cast<const i32x4_t*>(p + pos), *reinterpret_cast<const i32x4_t*>(p + pos4));
+  };
+  for (int q = q0, buffer = 0; q < q1; buffer ^= 1) {
+    const int qe = min(q + 4, q1), qs = q;
+    ask_token_scales(qe);
+    for (; q < qe; ++q) {
+      const uint32_t* const ts = reinterpret_cast<const uint32_t*>(token_scales + buffer * kTokens + r) + (q - qs);
+      const uint32_t* const rs = row_scale_words + (q & 1) * kRows + 16 * wave * RB + r;
+      int sw[RB];
 #pragma unroll
-    for (int t = 0; t < kTb; ++t) sx[t] = (int)scale[16 * t + r];
-#pragma unroll
-    for (int i = 0; i < RB; ++i) sw[i] = (int)scale[256 + 16 * (wave * RB + i) + r];
-    ask_scales(q + 1);
-    four([&](auto j) {
-      const int kt = 4 * q + j;
-      copy((j + 3) & 3, kt + 3);
-      weights((j + kAhead) % kSets, kt + kAhead);
-      __builtin_amdgcn_sched_barrier(0);        // the loads go out first,
-      const uint8_t* const cur = lds + j * kStage + pos;
-      i32x8_t b[2];
-      b[0] = load_halves(cur, 1024);
-#pragma unroll
-      for (int t = 0; t < kTb; ++t) {
-        if (t + 1 < kTb) b[(t + 1) & 1] = load_halves(cur + (t + 1) * kTile, 1024);
-#pragma unroll
-        for (int i = 0; i < RB; ++i) acc[i][t] = mfma8<j>(a[j % kSets][i], b[t & 1], acc[i][t], sw[i], sx[t]);
-        asm volatile("" ::: "memory");          // and an operand from LDS just before the products with the one before it
+      for (int i = 0; i < RB; ++i) sw[i] = (int)rs[16 * i];
+      ask_row_scales(q + 1);
+      four([&](auto j) {
+        const int kt = 4 * q + j;
+        weights((j + kAhead) % kSets, kt + kAhead);     // (before the copies: loads come back in order, and these are due first)
         __builtin_amdgcn_sched_barrier(0);
-      }
-      if constexpr (j == 2) put_scales(q + 1);
-      // the copies for the next step have arrived when no more is on its way than the two steps after them asked for
-      wait_loads<2 * (kCopies + 2 * RB)>();
-      lds_barrier();
-    }, std::make_integer_sequence<int, 4>{});
+        copy((j + 3) & 3, kt + 3);
+        __builtin_amdgcn_sched_barrier(0);        // the loads go out first,
+        const uint8_t* const cur = lds + j * kStage;
+        i32x8_t b[2];
+        int sx[2];
+        b[0] = operand(cur);
+        sx[0] = (int)ts[0];
+#pragma unroll
+        for (int t = 0; t < TB; ++t) {
+          if (t + 1 < TB) {
+            b[(t + 1) & 1] = operand(cur + (t + 1) * kTile);
+            sx[(t + 1) & 1] = (int)ts[64 * (t + 1)];
+          }
+#pragma unroll
+          for (int i = 0; i < RB; ++i) acc[i][t] = mfma8<j>(a[j % kSets][i], b[t & 1], acc[i][t], sw[i], sx[t & 1]);
+          asm volatile("" ::: "memory");          // and an operand from LDS just before the products with the one before it
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        if constexpr (j == 2) put_row_scales(q + 1);
+        // the copies for the next step have arrived when no more is on its way than the two steps after them asked for
+        wait_and_meet<2 * (kCopies + 2 * RB)>();
+      }, std::make_integer_sequence<int, 4>{});
+    }
+    put_token_scales(buffer ^ 1, q);
+    wait_and_meet<2 * (kCopies + 2 * RB)>();
   }
-  wait_loads<0>();      // no copy outlives the workgroup's LDS
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");      // no copy outlives the workgroup's LDS
   float* const slice = part ? part + (int64_t)blockIdx.y * M * w.N : nullptr;
 #pragma unroll
   for (int i = 0; i < RB; ++i) {
     const int64_t n = 16 * (int64_t)(rb0 + i) + 4 * g;
     if (n >= w.N) continue;
 #pragma unroll
-    for (int t = 0; t < kTb; ++t) {
+    for (int t = 0; t < TB; ++t) {
       const int64_t m = m0 + 16 * t + r;
       if (m >= M) continue;
       if (!slice) {
@@ -301,63 +332,94 @@ __global__ __launch_bounds__(256, 2) void k_tiled8(Rows8 x, int M, W8 w, _Float1
   }
 }
 
-// The splits' sums, added in their order.
-__global__ __launch_bounds__(256) void k_join8(const float* part, int splits, int64_t M, int64_t N, _Float16* y,
-                                               int64_t ys) {
-  const int64_t all = M * N;
-  for (int64_t o = (int64_t)blockIdx.x * 256 + threadIdx.x; o < all; o += (int64_t)gridDim.x * 256) {
-    float v = part[o];
-    for (int k = 1; k < splits; ++k) v += part[k * all + o];
-    const int64_t m = o / N;
-    y[m * ys + (o - m * N)] = (_Float16)v;
+// The splits' sums, added in their order: a workgroup takes 1024 outputs of a token.
+__global__ __launch_bounds__(256) void k_join8(const float* part, int splits, int64_t M, int64_t N, int per_row,
+                                               _Float16* y, int64_t ys) {
+  const int64_t m = blockIdx.x / per_row, n = 1024 * (int64_t)(blockIdx.x - m * per_row) + 4 * (int)threadIdx.x;
+  if (n >= N) return;
+  typedef float float4_any_t __attribute__((ext_vector_type(4), aligned(4)));
+  const float* p = part + m * N + n;
+  float4_t v = {0.f, 0.f, 0.f, 0.f};
+  for (int k = 0; k < splits; ++k, p += M * N) {
+    if (n + 4 <= N) {
+      v += *reinterpret_cast<const float4_any_t*>(p);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (n + i < N) v[i] += p[i];
+    }
   }
+  put4(y + m * ys + n, v, N - n);
 }
 
-template <int RB>
+template <int RB, int TB>
 hipError_t go_tiled(const Rows8& x, int64_t M, const W8& w, _Float16* y, int64_t ys, float* part,
                     const Linear8Plan& p, hipStream_t s) {
-  const int NT = (w.Nb + 4 * RB - 1) / (4 * RB), MT = (int)((M + 16 * kTb - 1) / (16 * kTb));
-  hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_tiled8<RB>),
-                                     hipFuncAttributeMaxDynamicSharedMemorySize, kTiledLds);
+  constexpr int kTokens = 16 * TB, kLds = tiled_lds(RB, kTokens);
+  const int NT = (w.Nb + 4 * RB - 1) / (4 * RB), MT = (int)((M + kTokens - 1) / kTokens);
+  hipError_t e = hipSuccess;
+  if (kLds > 65536)
+    e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_tiled8<RB, TB>), hipFuncAttributeMaxDynamicSharedMemorySize,
+                            kLds);
   if (e != hipSuccess) return e;
-  k_tiled8<RB><<<dim3((unsigned)(NT * MT), (unsigned)p.splits), dim3(256), kTiledLds, s>>>(x, (int)M, w, y, ys, part, NT,
-                                                                                           NT * MT, p.per);
+  k_tiled8<RB, TB><<<dim3((unsigned)(NT * MT), (unsigned)p.splits), dim3(256), kLds, s>>>(x, (int)M, w, y, ys, part, NT,
+                                                                                        NT * MT, p.per);
   e = hipGetLastError();
   if (e == hipSuccess && part) {
-    const int64_t groups = (M * w.N + 255) / 256;
-    k_join8<<<dim3((unsigned)(groups < 8192 ? groups : 8192)), dim3(256), 0, s>>>(part, p.splits, M, w.N, y, ys);
+    const int per_row = (int)((w.N + 1023) / 1024);
+    k_join8<<<dim3((unsigned)(M * per_row)), dim3(256), 0, s>>>(part, p.splits, M, w.N, per_row, y, ys);
     e = hipGetLastError();
   }
   return e;
 }
 
+// The tiled kernel's variants, and the time of a step of 128 columns on a CU that has nothing else, in us (MI355X, by 2 to 14
+// tiles a CU of 28672 x 8192; they are bound by what comes from L2, so a CU with two workgroups takes twice that).
+struct Variant {
+  int r, tb;
+  double step;
+};
+constexpr Variant kVariants[] = {{1, 2, 0.165}, {1, 4, 0.29}, {2, 2, 0.27}, {2, 4, 0.36}, {2, 8, 0.54}, {4, 8, 0.97}};
+
 }  // namespace
 
+// Up to 16 tokens the weights are streamed. Above, the variant with the least time by a model of what was measured over 17
+// to 2048 tokens, 1000 x 1000 to 28672 x 8192 (its choice is the fastest or within a tenth of it): 4 us to begin and end,
+// the steps of a CU's tiles one after the other, the weights from memory at 15 TB/s (what is left of it where the steps
+// cover the rest), and 5 us and the traffic of partial sums at 5 TB/s to join splits of K. Streamed: 3 us, the weights at
+// 5.2 TB/s and the tokens' codes, which each workgroup reads, at 13.
 Linear8Plan plan_linear8(int64_t M, int64_t N, int64_t K) {
-  Linear8Plan p = {};
+  Linear8Plan best = {};
   const int64_t Nb = (N + 15) / 16, Kt = (K + kQ8Block - 1) / kQ8Block, Kq = (Kt + 3) / 4;
-  p.splits = 1;
-  p.per = (int)(4 * Kq);
+  const double weights = (double)Nb * Kt * kTile;
+  double least = 1e30;
   if (M <= 64) {
-    p.nt = M <= 16 ? 1 : M <= 32 ? 2 : 4;
-    p.r = Nb >= 2048 ? 2 : 1;
-    p.waves = (int)(Kq < 8 ? Kq : 8);
-    p.groups = 2 * ((Nb + p.r - 1) / p.r);     // of 512 threads
-    return p;
+    best.nt = M <= 16 ? 1 : M <= 32 ? 2 : 4;
+    best.r = Nb >= 2048 ? 2 : 1;
+    best.waves = (int)(Kq < 8 ? Kq : 8);
+    best.groups = 2 * ((Nb + best.r - 1) / best.r);     // of 512 threads
+    least = 3.0 + weights / 5.2e6 + (double)Nb / best.r * 16.0 * best.nt * K / 13e6;
+    if (M <= 16) return best;
   }
-  const int64_t MT = (M + 16 * kTb - 1) / (16 * kTb);
-  p.r = ((Nb + 15) / 16) * MT >= 256 ? 4 : 2;
-  const int64_t T = ((Nb + 4 * p.r - 1) / (4 * p.r)) * MT;
-  if (T < 256) {
-    int64_t S = 512 / T;
-    S = S < Kq ? S : Kq;
-    const int64_t per = (Kq + S - 1) / S;
-    p.per = (int)(4 * per);
-    p.splits = (int)((Kq + per - 1) / per);
-    if (p.splits > 1) p.bytes = (size_t)p.splits * M * N * sizeof(float);
+  for (const Variant& v : kVariants) {
+    const int64_t T = ((Nb + 4 * v.r - 1) / (4 * v.r)) * ((M + 16 * v.tb - 1) / (16 * v.tb));
+    for (int64_t S : {1, 2, 3, 4, 8}) {
+      if (S > 1 && (S > Kq || T * S > 1024)) break;
+      const int64_t per = (Kq + S - 1) / S, splits = (Kq + per - 1) / per, a_cu = (T * splits + 255) / 256;
+      double t = 4.0 + 4.0 * per * a_cu * v.step + weights / 15e6;
+      if (splits > 1) t += 5.0 + 8.0 * splits * M * N / 5e6;
+      if (t >= least) continue;
+      least = t;
+      best = {};
+      best.r = v.r;
+      best.tb = v.tb;
+      best.splits = (int)splits;
+      best.per = (int)(4 * per);
+      best.groups = T * splits;
+      if (splits > 1) best.bytes = (size_t)splits * M * N * sizeof(float);
+    }
   }
-  p.groups = T * p.splits;
-  return p;
+  return best;
 }
 
 hipError_t launch_linear8(const Rows8& x, int64_t M, const W8& w, _Float16* y, int64_t ys, void* ws,
@@ -366,7 +428,14 @@ hipError_t launch_linear8(const Rows8& x, int64_t M, const W8& w, _Float16* y, i
   if (p.nt == 2) return p.r == 1 ? go_stream<2, 1>(x, M, w, y, ys, p, s) : go_stream<2, 2>(x, M, w, y, ys, p, s);
   if (p.nt == 4) return p.r == 1 ? go_stream<4, 1>(x, M, w, y, ys, p, s) : go_stream<4, 2>(x, M, w, y, ys, p, s);
   float* part = p.splits > 1 ? static_cast<float*>(ws) : nullptr;
-  return p.r == 4 ? go_tiled<4>(x, M, w, y, ys, part, p, s) : go_tiled<2>(x, M, w, y, ys, part, p, s);
+  switch (16 * p.r + p.tb) {
+    case 16 * 4 + 8: return go_tiled<4, 8>(x, M, w, y, ys, part, p, s);
+    case 16 * 2 + 8: return go_tiled<2, 8>(x, M, w, y, ys, part, p, s);
+    case 16 * 2 + 4: return go_tiled<2, 4>(x, M, w, y, ys, part, p, s);
+    case 16 * 2 + 2: return go_tiled<2, 2>(x, M, w, y, ys, part, p, s);
+    case 16 * 1 + 4: return go_tiled<1, 4>(x, M, w, y, ys, part, p, s);
+    default: return go_tiled<1, 2>(x, M, w, y, ys, part, p, s);
+  }
 }
 
 }  // namespace mq

@@ -506,8 +506,8 @@ def test_the_way_out_on_other_streams_at_once(hd):
 
 def test_workspaces_that_are_too_small_are_refused(hd):
     import torch
-    h = Head(hd, 100, 4096, 200)
-    c, s = hd.mq_quantize8(torch.zeros((100, 4096), dtype=torch.float16, device="cuda"))
+    h = Head(hd, 100, 40000, 64)                 # few outputs of long sums: split along K
+    c, s = hd.mq_quantize8(torch.zeros((100, 40000), dtype=torch.float16, device="cuda"))
     need = hd.linear8_workspace(h.layer, 100)
     assert need > 0
     with pytest.raises(hd.MQError):
