@@ -144,8 +144,8 @@ hipError_t go_stream(const Rows8& x, int64_t M, const W8& w, _Float16* y, int64_
 // what lies past K in the last four is zero in LDS and adds nothing. Nothing in
 // a step is under a condition: a load there would be waited for where the
 // branches meet.
-// codes; scales of the tokens, 16 blocks of each, and of the weight rows, 4 of each; each twice
-constexpr int tiled_lds(int rb, int tokens) { return 4 * tokens * kQ8Block + 2 * (16 * tokens + 4 * 64 * rb); }
+// codes; scales of the tokens, 8 blocks of each, and of the weight rows, 4 of each; each twice
+constexpr int tiled_lds(int rb, int tokens) { return 4 * tokens * kQ8Block + 2 * (8 * tokens + 4 * 64 * rb); }
 
 // The codes of 16 tokens x 128 columns in LDS are filled by two copies of 1 KiB, in lane order. Copy u, lane l brings row
 // 8 u + l / 8, chunk l % 8 ^ l / 8 of its 8 chunks of 16 bytes: eight lanes read a row's whole line (quads with runs of 64
@@ -175,8 +175,8 @@ __global__ __launch_bounds__(256, 2) void k_tiled8(Rows8 x, int M, W8 w, _Float1
   constexpr int kSets = kAhead + 1;
   constexpr int kCopies = TB / 2;              // of a wave in a step
   constexpr int kTokens = 16 * TB, kRows = 64 * RB, kStage = kTokens * kQ8Block;
-  uint4* const token_scales = reinterpret_cast<uint4*>(lds + 4 * kStage);
-  uint32_t* const row_scale_words = reinterpret_cast<uint32_t*>(lds + 4 * kStage + 2 * 16 * kTokens);
+  uint2* const token_scales = reinterpret_cast<uint2*>(lds + 4 * kStage);
+  uint32_t* const row_scale_words = reinterpret_cast<uint32_t*>(lds + 4 * kStage + 2 * 8 * kTokens);
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int r = lane & 15, g = lane >> 4;
   const int tile = xcd_tile(blockIdx.x, T), MT = T / NT;
@@ -215,37 +215,29 @@ __global__ __launch_bounds__(256, 2) void k_tiled8(Rows8 x, int M, W8 w, _Float1
                        __builtin_bit_cast(i32x4_t, __builtin_amdgcn_raw_buffer_load_b128(wr, wl, at + 1024, 0)));
     }
   };
-  // The scales: a thread asks for 16 of a token's at a time, once in 16 steps (64 tokens are 64 lines: asked for by fours
-  // they were a sixth of all that came from L2), and for a word of a weight row's, four of them, once in 4; into LDS later.
-  // A token's 16 bytes are taken from where they lie, or, where that would pass the end of all scales, from some bytes before
-  // and shifted; bytes past the row count as 127 (their codes are zero, but a NaN there would not be).
+  // The scales: a thread asks for 8 of a token's at a time, once in 8 steps (128 tokens are 128 lines: asked for by fours
+  // they were a sixth of all that came from L2; 16 at a time spilled registers that had to wait for them), and for a word of
+  // a weight row's, four of them, once in 4; into LDS later. A token's 8 bytes are taken from where they lie, or, where that
+  // would pass the end of all scales, from some bytes before and shifted; bytes past the row count as 127 (their codes are
+  // zero, but a NaN there would not be).
   const uint8_t* const xs = x.scales + (int64_t)m0 * x.sstride;
   const int xs_own = min(tid % kTokens, M - 1 - m0) * (int)x.sstride;
-  const int xs_last = (int)min((int64_t)0x40000000, (M - 1 - m0) * x.sstride + w.Kt - 16);
+  const int xs_last = (int)min((int64_t)0x40000000, (M - 1 - m0) * x.sstride + w.Kt - 8);
   const __amdgpu_buffer_rsrc_t wsr = __builtin_amdgcn_make_buffer_rsrc(
       const_cast<uint8_t*>(w.scales + (int64_t)64 * min(nt * 4 * RB, w.Nb - 1) * w.Kq), 0, 0x7FFFFFFF, kBufferRaw);
   const int ws_own = 64 * min(tid % kRows >> 4, w.Nb - 1 - min(nt * 4 * RB, w.Nb - 1)) * w.Kq + 4 * (tid & 15);
-  typedef unsigned __int128 u128;
-  u128 token_bytes;
-  int token_over;
+  uint64_t token_bytes;
   uint32_t row_word;
+  auto token_over = [&](int q) { return max(0, xs_own + 4 * min(q, w.Kq - 1) - xs_last); };
   auto ask_token_scales = [&](int q) {
-    const int at = xs_own + 4 * min(q, w.Kq - 1);
-    token_over = max(0, at - xs_last);
-    typedef u128 u128_any_t __attribute__((aligned(1)));
-    token_bytes = *reinterpret_cast<const u128_any_t*>(xs + (at - token_over));
+    typedef uint64_t u64_any_t __attribute__((aligned(1)));
+    token_bytes = *reinterpret_cast<const u64_any_t*>(xs + (xs_own + 4 * min(q, w.Kq - 1) - token_over(q)));
   };
   auto put_token_scales = [&](int buffer, int q) {
-    const u128 v = token_bytes >> (8 * token_over);
-    const int have = w.Kt - 4 * min(q, w.Kq - 1);
-    uint32_t to[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int n = min(max(have - 4 * i, 0), 4);
-      const uint32_t own = n == 4 ? 0xFFFFFFFFu : (1u << (8 * n)) - 1;
-      to[i] = ((uint32_t)(v >> (32 * i)) & own) | (0x7F7F7F7Fu & ~own);
-    }
-    token_scales[buffer * kTokens + tid % kTokens] = make_uint4(to[0], to[1], to[2], to[3]);
+    const uint64_t v = token_bytes >> (8 * token_over(q));
+    const int have = min(w.Kt - 4 * min(q, w.Kq - 1), 8);
+    const uint64_t own = ~0ull >> (8 * (8 - have)), u = (v & own) | (0x7F7F7F7F7F7F7F7Full & ~own);
+    token_scales[buffer * kTokens + tid % kTokens] = make_uint2((uint32_t)u, (uint32_t)(u >> 32));
   };
   auto ask_row_scales = [&](int q) { row_word = __builtin_amdgcn_raw_buffer_load_b32(wsr, ws_own, 64 * min(q, w.Kq - 1), 0); };
   auto put_row_scales = [&](int q) { row_scale_words[(q & 1) * kRows + tid % kRows] = row_word; };
@@ -271,7 +263,7 @@ __global__ __launch_bounds__(256, 2) void k_tiled8(Rows8 x, int M, W8 w, _Float1
     return join(*reinterpret_cast<const i32x4_t*>(p + pos), *reinterpret_cast<const i32x4_t*>(p + pos4));
   };
   for (int q = q0, buffer = 0; q < q1; buffer ^= 1) {
-    const int qe = min(q + 4, q1), qs = q;
+    const int qe = min(q + 2, q1), qs = q;
     ask_token_scales(qe);
     for (; q < qe; ++q) {
       const uint32_t* const ts = reinterpret_cast<const uint32_t*>(token_scales + buffer * kTokens + r) + (q - qs);
@@ -295,7 +287,7 @@ __global__ __launch_bounds__(256, 2) void k_tiled8(Rows8 x, int M, W8 w, _Float1
         for (int t = 0; t < TB; ++t) {
           if (t + 1 < TB) {
             b[(t + 1) & 1] = operand(cur + (t + 1) * kTile);
-            sx[(t + 1) & 1] = (int)ts[64 * (t + 1)];
+            sx[(t + 1) & 1] = (int)ts[32 * (t + 1)];
           }
 #pragma unroll
           for (int i = 0; i < RB; ++i) acc[i][t] = mfma8<j>(a[j % kSets][i], b[t & 1], acc[i][t], sw[i], sx[t & 1]);
@@ -384,7 +376,7 @@ constexpr Variant kVariants[] = {{1, 2, 0.165}, {1, 4, 0.29}, {2, 2, 0.27}, {2, 
 }  // namespace
 
 // Up to 16 tokens the weights are streamed. Above, the variant with the least time by a model of what was measured over 17
-// to 2048 tokens, 1000 x 1000 to 28672 x 8192 (its choice is the fastest or within a tenth of it): 4 us to begin and end,
+// to 2048 tokens, 1000 x 1000 to 28672 x 8192 (its choice is the fastest or within a fifth of it): 4 us to begin and end,
 // the steps of a CU's tiles one after the other, the weights from memory at 15 TB/s (what is left of it where the steps
 // cover the rest), and 5 us and the traffic of partial sums at 5 TB/s to join splits of K. Streamed: 3 us, the weights at
 // 5.2 TB/s and the tokens' codes, which each workgroup reads, at 13.
@@ -393,8 +385,8 @@ Linear8Plan plan_linear8(int64_t M, int64_t N, int64_t K) {
   const int64_t Nb = (N + 15) / 16, Kt = (K + kQ8Block - 1) / kQ8Block, Kq = (Kt + 3) / 4;
   const double weights = (double)Nb * Kt * kTile;
   double least = 1e30;
-  if (M <= 64) {
-    best.nt = M <= 16 ? 1 : M <= 32 ? 2 : 4;
+  if (M <= 32) {
+    best.nt = M <= 16 ? 1 : 2;
     best.r = Nb >= 2048 ? 2 : 1;
     best.waves = (int)(Kq < 8 ? Kq : 8);
     best.groups = 2 * ((Nb + best.r - 1) / best.r);     // of 512 threads
@@ -426,7 +418,6 @@ hipError_t launch_linear8(const Rows8& x, int64_t M, const W8& w, _Float16* y, i
                           const Linear8Plan& p, hipStream_t s) {
   if (p.nt == 1) return p.r == 1 ? go_stream<1, 1>(x, M, w, y, ys, p, s) : go_stream<1, 2>(x, M, w, y, ys, p, s);
   if (p.nt == 2) return p.r == 1 ? go_stream<2, 1>(x, M, w, y, ys, p, s) : go_stream<2, 2>(x, M, w, y, ys, p, s);
-  if (p.nt == 4) return p.r == 1 ? go_stream<4, 1>(x, M, w, y, ys, p, s) : go_stream<4, 2>(x, M, w, y, ys, p, s);
   float* part = p.splits > 1 ? static_cast<float*>(ws) : nullptr;
   switch (16 * p.r + p.tb) {
     case 16 * 4 + 8: return go_tiled<4, 8>(x, M, w, y, ys, part, p, s);
