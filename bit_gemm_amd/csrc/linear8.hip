@@ -60,26 +60,42 @@ __device__ __forceinline__ void four(F&& f, std::integer_sequence<int, J...>) {
   (f(std::integral_constant<int, J>{}), ...);
 }
 
+// The codes of 16 tokens x 128 columns in LDS are filled by two copies of 1 KiB, in lane order. Copy u, lane l brings row
+// 8 u + l / 8, chunk l % 8 ^ l / 8 of its 8 chunks of 16 bytes: eight lanes read a row's whole line (quads with runs of 64
+// bytes ask for each line twice: X took twice the time of as many bytes of weights), and the 8 lanes that LDS serves at once
+// when the operand is read back (rows n .. n + 7, one chunk) find 8 different banks of 16 bytes.
+__device__ __forceinline__ uint32_t stage_from(int lane, uint32_t stride) {
+  return (uint32_t)(lane >> 3) * stride + 16u * (uint32_t)((lane & 7) ^ (lane >> 3));
+}
+// Where lane n + 16 g finds chunk g of row n; chunk 4 + g lies 64 bytes away from it, up or down.
+__device__ __forceinline__ uint32_t stage_pos(int lane) {
+  const int n = lane & 15, g = lane >> 4;
+  return 16u * (uint32_t)(8 * n + (g ^ (n & 7)));
+}
+
 // ------------------------------------------------------------ few tokens
 // Up to 16 NT tokens: a workgroup takes R blocks of 16 weight rows, its waves
 // fours of tiles along K in turn (a lane's scales of four blocks are one word).
 // The weights go from memory straight to the registers that the instruction
-// reads, once; the tokens' codes come through L2. The waves' sums meet in LDS
-// and are added in their order.
+// reads, once. The tokens' codes come from L2 through a part of LDS that is the
+// wave's own: read in the operand's order they are 16 rows an instruction, in
+// pieces of 16 bytes (16 tokens, 11008 x 4096: 12.1 us so, 10.0 through LDS).
+// The waves' sums meet in LDS and are added in their order.
 template <int NT, int R>
 __global__ __launch_bounds__(512) void k_stream8(Rows8 x, int M, W8 w, _Float16* y, int64_t ys) {
-  extern __shared__ float4_t red[];
+  extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int waves = blockDim.x >> 6;
-  const int r = lane & 15, g = lane >> 4;
+  const int r = lane & 15;
   const int rb0 = blockIdx.x * R;
-  const uint8_t *xc[NT], *xs[NT];
+  uint8_t* const own = lds + wave * (4 * NT * kTile);
+  const __amdgpu_buffer_rsrc_t xr =      // reads past the tokens' rows give zero
+      __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(x.codes), 0, (int)(M * x.stride), kBufferRaw);
+  const uint32_t xl = stage_from(lane, (uint32_t)x.stride);
+  const uint8_t* xs[NT];
 #pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    const int64_t m = min(16 * t + r, M - 1);      // tokens past the last one repeat it; their outputs are not stored
-    xc[t] = x.codes + m * x.stride + 16 * g;
-    xs[t] = x.scales + m * x.sstride;
-  }
+  for (int t = 0; t < NT; ++t) xs[t] = x.scales + (int64_t)min(16 * t + r, M - 1) * x.sstride;
+  const uint32_t pos = stage_pos(lane), pos4 = pos ^ 64;
   float4_t acc[R][NT];
 #pragma unroll
   for (int i = 0; i < R; ++i)
@@ -87,8 +103,19 @@ __global__ __launch_bounds__(512) void k_stream8(Rows8 x, int M, W8 w, _Float16*
     for (int t = 0; t < NT; ++t) acc[i][t] = float4_t{0.f, 0.f, 0.f, 0.f};
 
   for (int q = wave; q < w.Kq; q += waves) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+          __builtin_amdgcn_raw_ptr_buffer_load_lds(
+              xr, (__attribute__((address_space(3))) void*)(own + (j * NT + t) * kTile + 1024 * u), 16,
+              xl + (uint32_t)(16 * t + 8 * u) * (uint32_t)x.stride + (uint32_t)(min(4 * q + j, w.Kt - 1) * kQ8Block), 0, 0, 0);
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
     int sw[R], sx[NT];
-    i32x8_t a[4][R], b[4][NT];
+    i32x8_t a[4][R];
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       const int64_t rb = min(rb0 + i, w.Nb - 1);
@@ -100,20 +127,27 @@ __global__ __launch_bounds__(512) void k_stream8(Rows8 x, int M, W8 w, _Float16*
       }
     }
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      sx[t] = row_scales(xs[t], q, w.Kt);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) b[j][t] = load_halves(xc[t] + kQ8Block * min(4 * q + j, w.Kt - 1), 64);
-    }
+    for (int t = 0; t < NT; ++t) sx[t] = row_scales(xs[t], q, w.Kt);
+    asm volatile("s_waitcnt vmcnt(%0)" ::"n"(8 * R) : "memory");      // the copies, which were asked for before 8 R loads
     four([&](auto j) {
       if (4 * q + j < w.Kt) {
+        i32x8_t b[NT];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          const uint8_t* const from = own + (j * NT + t) * kTile;
+          b[t] = join(*reinterpret_cast<const i32x4_t*>(from + pos), *reinterpret_cast<const i32x4_t*>(from + pos4));
+        }
 #pragma unroll
         for (int i = 0; i < R; ++i)
 #pragma unroll
-          for (int t = 0; t < NT; ++t) acc[i][t] = mfma8<j>(a[j][i], b[j][t], acc[i][t], sw[i], sx[t]);
+          for (int t = 0; t < NT; ++t) acc[i][t] = mfma8<j>(a[j][i], b[t], acc[i][t], sw[i], sx[t]);
       }
     }, std::make_integer_sequence<int, 4>{});
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");                // before the next copies land where these were read
   }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  __syncthreads();
+  float4_t* const red = reinterpret_cast<float4_t*>(lds);
 #pragma unroll
   for (int i = 0; i < R; ++i)
 #pragma unroll
@@ -131,7 +165,12 @@ __global__ __launch_bounds__(512) void k_stream8(Rows8 x, int M, W8 w, _Float16*
 template <int NT, int R>
 hipError_t go_stream(const Rows8& x, int64_t M, const W8& w, _Float16* y, int64_t ys, const Linear8Plan& p,
                      hipStream_t s) {
-  const size_t lds = (size_t)p.waves * R * NT * 1024;
+  const int lds = p.waves * 4 * NT * kTile;      // the tokens' codes, later the sums (R is 2 at most)
+  static_assert(R * 1024 <= 4 * kTile, "the sums of a wave fit where its codes were");
+  hipError_t e = hipSuccess;
+  if (lds > 65536)
+    e = hipFuncSetAttribute(reinterpret_cast<const void*>(&k_stream8<NT, R>), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+  if (e != hipSuccess) return e;
   k_stream8<NT, R><<<dim3((unsigned)((w.Nb + R - 1) / R)), dim3(64 * p.waves), lds, s>>>(x, (int)M, w, y, ys);
   return hipGetLastError();
 }
@@ -146,19 +185,6 @@ hipError_t go_stream(const Rows8& x, int64_t M, const W8& w, _Float16* y, int64_
 // branches meet.
 // codes; scales of the tokens, 8 blocks of each, and of the weight rows, 4 of each; each twice
 constexpr int tiled_lds(int rb, int tokens) { return 4 * tokens * kQ8Block + 2 * (8 * tokens + 4 * 64 * rb); }
-
-// The codes of 16 tokens x 128 columns in LDS are filled by two copies of 1 KiB, in lane order. Copy u, lane l brings row
-// 8 u + l / 8, chunk l % 8 ^ l / 8 of its 8 chunks of 16 bytes: eight lanes read a row's whole line (quads with runs of 64
-// bytes ask for each line twice: X took twice the time of as many bytes of weights), and the 8 lanes that LDS serves at once
-// when the operand is read back (rows n .. n + 7, one chunk) find 8 different banks of 16 bytes.
-__device__ __forceinline__ uint32_t stage_from(int lane, uint32_t stride) {
-  return (uint32_t)(lane >> 3) * stride + 16u * (uint32_t)((lane & 7) ^ (lane >> 3));
-}
-// Where lane n + 16 g finds chunk g of row n; chunk 4 + g lies 64 bytes away from it, up or down.
-__device__ __forceinline__ uint32_t stage_pos(int lane) {
-  const int n = lane & 15, g = lane >> 4;
-  return 16u * (uint32_t)(8 * n + (g ^ (n & 7)));
-}
 
 // Waits until no more than N loads are on their way, and for the wave's own LDS accesses, then for the other waves. (A fence
 // would wait for every copy into LDS, also for those that the next steps need.)
@@ -379,7 +405,10 @@ constexpr Variant kVariants[] = {{1, 2, 0.165}, {1, 4, 0.29}, {2, 2, 0.27}, {2, 
 // to 2048 tokens, 1000 x 1000 to 28672 x 8192 (its choice is the fastest or within a fifth of it): 4 us to begin and end,
 // the steps of a CU's tiles one after the other, the weights from memory at 15 TB/s (what is left of it where the steps
 // cover the rest), and 5 us and the traffic of partial sums at 5 TB/s to join splits of K. Streamed: 3 us, the weights at
-// 5.2 TB/s and the tokens' codes, which each workgroup reads, at 13.
+// 5.2 TB/s and the tokens' codes, which each workgroup reads, at 60, by two blocks of weight rows where by one it would be
+// more workgroups than CUs (LDS holds one workgroup of 32 tokens: 6144 x 6144 10.4 us by two, 12.7 by one; 4096 x 4096 7.2
+// and 6.7), and up to 16 tokens where by two it is four a CU (8 tokens, 65536 x 2048: 24.8 and 25.5; 28672 x 8192: 44.5
+// and 42.2).
 Linear8Plan plan_linear8(int64_t M, int64_t N, int64_t K) {
   Linear8Plan best = {};
   const int64_t Nb = (N + 15) / 16, Kt = (K + kQ8Block - 1) / kQ8Block, Kq = (Kt + 3) / 4;
@@ -387,10 +416,10 @@ Linear8Plan plan_linear8(int64_t M, int64_t N, int64_t K) {
   double least = 1e30;
   if (M <= 32) {
     best.nt = M <= 16 ? 1 : 2;
-    best.r = Nb >= 2048 ? 2 : 1;
+    best.r = Nb > (M <= 16 ? 2047 : 256) ? 2 : 1;
     best.waves = (int)(Kq < 8 ? Kq : 8);
     best.groups = 2 * ((Nb + best.r - 1) / best.r);     // of 512 threads
-    least = 3.0 + weights / 5.2e6 + (double)Nb / best.r * 16.0 * best.nt * K / 13e6;
+    least = 3.0 + weights / 5.2e6 + (double)Nb / best.r * 16.0 * best.nt * K / 60e6;
     if (M <= 16) return best;
   }
   for (const Variant& v : kVariants) {
