@@ -456,6 +456,24 @@ def _rows8(codes, scales, device: int, tokens: int, width: int):
     return cp, cs, sp, ss
 
 
+def _rows8_out(codes, scales, x, other, device: int):
+    """The 8-bit rows that a call writes for x [tokens, width], made where they are not given; addresses and strides."""
+    M, W = x.shape
+    n = (W + 127) // 128
+    if codes is None:        # by empty_like where it is x's shape (0.5 us faster)
+        codes = (_new(other, torch.empty_like, x, dtype=_E4M3) if W == 128 * n and x.is_contiguous() else
+                 _new(other, torch.empty, (M, 128 * n), dtype=_E4M3, device=x.device))
+        cp, cs = codes.data_ptr(), 128 * n
+    else:
+        cp, cs = _matrix(codes, "codes", device, _E4M3, (M, 128 * n))
+    if scales is None:
+        scales = _new(other, torch.empty, (M, n), dtype=_E8M0, device=x.device)
+        sp, ss = scales.data_ptr(), n
+    else:
+        sp, ss = _matrix(scales, "scales", device, _E8M0, (M, n))
+    return codes, scales, cp, cs, sp, ss
+
+
 def mq_norm_residual_q8(y, r, w_pre, w_post=None, gate=None, alpha: float = 1.0, beta: float = 1.0, eps: float = 1e-6,
                         weight_offset: float = 0.0, r_out=None, codes_out=None, scales_out=None, stream=None):
     """(r', codes, scales): mq_norm_residual with h = norm(r') (w_pre + offset) as 8-bit rows, for head.mq_linear8.
@@ -479,12 +497,7 @@ def mq_norm_residual_q8(y, r, w_pre, w_post=None, gate=None, alpha: float = 1.0,
     else:
         r_out = r
     wpre = _vector(w_pre, "w_pre", device, W)
-    n = (W + 127) // 128
-    if codes_out is None:
-        codes_out = _new(other, torch.empty, (M, 128 * n), dtype=_E4M3, device=r.device)
-    if scales_out is None:
-        scales_out = _new(other, torch.empty, (M, n), dtype=_E8M0, device=r.device)
-    cp, cs, sp, ss = _rows8(codes_out, scales_out, device, M, W)
+    codes_out, scales_out, cp, cs, sp, ss = _rows8_out(codes_out, scales_out, r, other, device)
     if M == 0:
         return r_out, codes_out, scales_out
     a = _norm_args(yp, r.data_ptr(), gp, wpost, wpre, rp, cp, M, W, ys, r.stride(0) if M > 1 else W, gs, rs, cs, alpha,

@@ -24,7 +24,7 @@ import struct
 
 import torch
 
-from .block import _apart, _current_device, _device, _E4M3, _E8M0, _F16, _matrix, _rows8, _stream
+from .block import _apart, _current_device, _device, _E4M3, _E8M0, _F16, _matrix, _rows8, _rows8_out, _stream
 from .mosaicq import MQError, _check, _new, _other
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -84,13 +84,8 @@ def mq_quantize8(x, codes_out=None, scales_out=None, stream=None):
     if device != _current_device():
         with torch.cuda.device(device):
             return mq_quantize8(x, codes_out, scales_out, stream)
-    n = (K + 127) // 128
     other = None if stream is None else _other(stream, x.device)
-    if codes_out is None:
-        codes_out = _new(other, torch.empty, (M, 128 * n), dtype=_E4M3, device=x.device)
-    if scales_out is None:
-        scales_out = _new(other, torch.empty, (M, n), dtype=_E8M0, device=x.device)
-    cp, cs, sp, ss = _rows8(codes_out, scales_out, device, M, K)
+    codes_out, scales_out, cp, cs, sp, ss = _rows8_out(codes_out, scales_out, x, other, device)
     if M:
         code = lib.mq_quantize8(x.data_ptr(), M, K, xs, cp, cs, sp, ss, _stream(stream, device))
         if code:
@@ -119,6 +114,7 @@ class Packed8:
         self._c = _W8(codes.data_ptr(), scales.data_ptr(), self.N, self.K)
         self._ref = ctypes.addressof(self._c)
         self._ws = {}      # tokens -> workspace bytes
+        self._like = codes.new_empty(0, dtype=_F16)
 
 
 def mq_pack8(W, stream=None) -> Packed8:
@@ -173,7 +169,7 @@ def mq_linear8(codes, scales, p: Packed8, out=None, workspace=None, stream=None)
     cp, cs, sp, ss = _rows8(codes, scales, device, M, p.K)
     other = None if stream is None else _other(stream, codes.device)
     if out is None:
-        out = _new(other, torch.empty, (M, p.N), dtype=_F16, device=codes.device)
+        out = _new(other, p._like.new_empty, (M, p.N))
         yp, ys = out.data_ptr(), p.N
     else:
         yp, ys = _matrix(out, "out", device, _F16, (M, p.N))
@@ -228,15 +224,15 @@ def mq_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, t
     R, V = logits.shape
     f32 = torch.float32
     other = None if stream is None else _other(stream, logits.device)
-    up = _setting(u, "u", device, f32, R)
-    if not up and R:
+    if u is None:
         raise TypeError("u must be a float32 tensor")
+    up = _setting(u, "u", device, f32, R)
     settings = (_setting(temperature, "temperature", device, f32, R), _setting(top_k, "top_k", device, torch.int32, R),
                 _setting(top_p, "top_p", device, f32, R), _setting(min_p, "min_p", device, f32, R))
     if token_out is None:
-        token_out = _new(other, torch.empty, R, dtype=torch.int32, device=logits.device)
+        token_out = _new(other, torch.empty_like, u, dtype=torch.int32)
     if logprob_out is None:
-        logprob_out = _new(other, torch.empty, R, dtype=f32, device=logits.device)
+        logprob_out = _new(other, torch.empty_like, u)
     tp, lp = _setting(token_out, "token_out", device, torch.int32, R), _setting(logprob_out, "logprob_out", device, f32, R)
     if R == 0:
         return token_out, logprob_out
