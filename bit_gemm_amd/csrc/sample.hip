@@ -60,7 +60,7 @@ struct Eight {
 };
 
 // f(v, at, s) of the wave's pieces s = first, first + step .. < end of 512 tokens each, 8 a lane. Four are asked for before
-// the first is used: a wave that waits for each by itself spends its time on that (256 rows of 50257: 24 us, so 17).
+// the first is used: a wave that waits for each by itself spends its time on that (256 rows of 50257: 24.3 us, so 23.6).
 template <typename T, typename F>
 __device__ __forceinline__ void each_piece(const T* row, int vocab, int first, int end, int step, F&& f) {
   const int lane = threadIdx.x & 63;
@@ -107,11 +107,11 @@ __device__ __forceinline__ double fma_c(double a, double b, double c) {
 // the first from a table of 256 and an exponent, the second the series of exp to the fourth power (the rest is under 2^-54,
 // |r| <= 1/2). Adding 2^52 leaves the whole number in the low bits. No branch, so that a thread's eight run side by side:
 // each by itself is a chain of 13 dependent fp64 steps. What lies beyond 2^-43 of the largest counts as that far, and gives
-// 0. (With a table of 32 and the sixth power, the constants copied: 64 x 131072 51 us, so 45.)
+// 0. (With a table of 32 and the sixth power, the constants copied: 64 x 131072 51 us, so 49.)
 constexpr int kTable = 256;
 struct Weigher {
   double top, scale;
-  const double* table;     // 2^(i / 256), in LDS
+  const double* table;     // 2^(40 + i / 256), in LDS
   __device__ __forceinline__ u64 operator()(float l) const {
     const double y = fmax(((double)l - top) * scale, -43.0 * kTable);
     const double n = rint(y), r = y - n;
@@ -121,13 +121,13 @@ struct Weigher {
     p = fma_c(p, r, c);
     p = fma(p, r, 1.0);
     const int k = (int)n;
-    const double w = ldexp(p * table[k & (kTable - 1)], (k >> 8) + 40) + 4503599627370496.0;
+    const double w = ldexp(p * table[k & (kTable - 1)], k >> 8) + 4503599627370496.0;
     return __builtin_bit_cast(u64, w) & 0xFFFFFFFFFFFFFull;
   }
 };
 // Fills the table; the caller's next barrier publishes it.
 __device__ __forceinline__ void fill_table(double* table) {
-  if (threadIdx.x < kTable) table[threadIdx.x] = exp2((double)threadIdx.x / kTable);
+  if (threadIdx.x < kTable) table[threadIdx.x] = kOne * exp2((double)threadIdx.x / kTable);
 }
 
 // floor(f total), f in 0 .. 1 taken to 31 bits, at most `most` steps of 2^-31; total < 2^62.
@@ -428,38 +428,91 @@ struct Lds {
   int i, n1;
 };
 
-// The n places in order. Few: each thread counts the places before its own and puts them there: n steps that do not wait for
-// each other, as the 45 of the network for 512 do (64 rows, 320 places in most: k_pick 17 us by the network).
-constexpr int kCounted = 512;
+// The n places in order. Few: a thread counts those before its own. More: the steps that they come from are cut again, into
+// as many equal parts as kBins allows; the places are put down by parts, and then each in its part, by counting those of it
+// before it (64 rows of up to 700 places: k_pick 16.4 us by counting among all up to 512 and a network beyond, so 10.9; 16
+// rows of some 200: 8.1 us by counting, 9.6 by parts). Where a part holds more than kEqual (equal logits), a network sorts
+// them all.
+constexpr int kFew = 256;
+constexpr uint32_t kEqual = 256;
 template <int THREADS>
-__device__ __forceinline__ void sort_places(u64* p, int n) {
-  constexpr int kPer = kCounted / THREADS;
+__device__ __forceinline__ void sort_places(Lds& s, const Row& x, const Limits& z, int n) {
+  constexpr int kPer = kList / THREADS, kCounts = kBins / THREADS;
   const int tid = threadIdx.x;
-  if (n <= kCounted) {
-    u64 mine[kPer];
-    int at[kPer];
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      mine[i] = THREADS * i + tid < n ? p[THREADS * i + tid] : ~0ull;
-      at[i] = 0;
-    }
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      if (THREADS * i + (tid & ~63) < n) {
+  u64* const p = s.place;
+  if (n <= kFew) {
+    const u64 mine = tid < n ? p[tid] : ~0ull;
+    int at = 0;
+    if ((tid & ~63) < n) {
 #pragma unroll 8
-        for (int e = 0; e < n; ++e) at[i] += p[e] < mine[i];
+      for (int e = 0; e < n; ++e) at += p[e] < mine;
+    }
+    __syncthreads();
+    if (tid < n) p[at] = mine;
+    __syncthreads();
+    return;
+  }
+  const bool gap = z.k > z.p1 && z.k < kBins;
+  const int steps = z.p1 - z.p0 + 1, per = kBins / (steps + gap);
+  auto part_of = [&](u64 place) {
+    const float t = fmaf(logit_at(place), -0.5f, 0.5f * x.top) * x.step;
+    const int b = (int)t;
+    return (b <= z.p1 ? b - z.p0 : steps) * per + min((int)((t - (float)b) * (float)per), per - 1);
+  };
+#pragma unroll
+  for (int i = 0; i < kCounts; ++i) s.count[THREADS * i + tid] = 0;
+  __syncthreads();
+  u64 mine[kPer];
+  uint32_t slot[kPer];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int e = THREADS * i + tid;
+    if (e < n) {
+      mine[i] = p[e];
+      slot[i] = atomicAdd(&s.count[part_of(mine[i])], 1u);
+    }
+  }
+  __syncthreads();
+  uint32_t c[kCounts], sum = 0, most = 0;
+#pragma unroll
+  for (int i = 0; i < kCounts; ++i) {
+    c[i] = s.count[kCounts * tid + i];
+    sum += c[i];
+    most = max(most, c[i]);
+  }
+  u64 all;
+  uint32_t before = (uint32_t)scan_group<THREADS / 64>(sum, s.scan, &all) - sum;
+  if (!__syncthreads_or(most > kEqual)) {
+#pragma unroll
+    for (int i = 0; i < kCounts; ++i) {
+      s.count[kCounts * tid + i] = before;
+      before += c[i];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kPer; ++i)
+      if (THREADS * i + tid < n) p[s.count[part_of(mine[i])] + slot[i]] = mine[i];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int e = THREADS * i + tid;
+      if (e < n) {
+        mine[i] = p[e];
+        const int part = part_of(mine[i]), end = part + 1 < kBins ? (int)s.count[part + 1] : n;
+        slot[i] = s.count[part];
+        for (int o = (int)slot[i]; o < end; ++o) slot[i] += p[o] < mine[i];
       }
     }
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kPer; ++i)
-      if (THREADS * i + tid < n) p[at[i]] = mine[i];
+      if (THREADS * i + tid < n) p[slot[i]] = mine[i];
     __syncthreads();
     return;
   }
   // Pairs in a network: a wave's 64 pairs are 128 places that follow each other while partners are up to 64 apart, and
   // those steps need the wave alone, and no barrier.
-  int n2 = 2 * kCounted;
+  int n2 = 2 * (int)kEqual;
   while (n2 < n) n2 <<= 1;
   for (int e = n + tid; e < n2; e += THREADS) p[e] = ~0ull;
   bool alone = false;        // whether the last step was the wave's own
@@ -498,7 +551,7 @@ __device__ __forceinline__ u64 end_of_list(Lds& s, const Row& x, const Limits& z
     s.i = 0;
     s.n1 = 0;
   }
-  sort_places<THREADS>(s.place, n);
+  sort_places<THREADS>(s, x, z, n);
   // The first n1 are the steps from p0 to p1; the others, behind a gap, step k. Sums of the weights before each.
   const bool gap = z.k > z.p1 && z.k < kBins;
   u64 sum = 0;
@@ -969,7 +1022,8 @@ __global__ __launch_bounds__(kPick) void k_pick(mq_sample_args a, Work w) {
 
 // ------------------------------------------------------------------- the host
 // Segments of a row, of 512 tokens at least: so many that about kGroups workgroups share the rows, and a wave's lanes can
-// hold what each workgroup of a row found.
+// hold what each workgroup of a row found. (With 256 workgroups 64 x 131072 takes 49 us, so 43.5; 16 x 131072 28.7 and 30.4:
+// there the joining of 32 histograms a row takes half of k_weigh.)
 constexpr int64_t kGroups = 512;
 
 void split(int64_t rows, int64_t vocab, int* splits, int* span) {

@@ -345,6 +345,26 @@ def test_sample_of_ties_takes_the_lower_index_first(hd, V):
     assert max(got) < -(-V // 2)
 
 
+@pytest.mark.parametrize("V", [6000, 40000])
+def test_sample_where_limits_end_in_long_runs(hd, V):
+    """Hundreds of tokens around a limit, in runs of equal logits of 1 to 1500, spread over the row."""
+    r = np.random.RandomState(12)
+    R, N = 24, 2000
+    l = np.full((R, V), -9.0, np.float32)
+    k = np.zeros(R, int)
+    for i in range(R):
+        longest = [1, 3, 40, 255, 256, 257, 600, 1500][i % 8]
+        runs, values = [], []
+        while sum(runs) < N:
+            runs.append(int(r.randint(1, longest + 1)))
+        values = np.repeat(2.0 - np.arange(len(runs)) * 2.0 ** -11 * (1 if i < 12 else 16), runs)[:N]
+        l[i, r.permutation(V)[:N]] = values
+        k[i] = r.randint(1, N) if i % 3 else 0
+    p = r.choice([0.3, 0.8, 1.0], R)
+    check_rows(hd, dev(l), r.rand(R).astype(np.float32), [1.0] * 12 + [0.25] * 12, k, p)
+    check_rows(hd, dev(l).half(), r.rand(R).astype(np.float32), [1.0] * 12 + [0.25] * 12, k, p)
+
+
 def test_sample_where_every_logit_falls_into_a_narrow_range(hd):
     """Float32 logits that differ in their last bits, around values of any size."""
     r = np.random.RandomState(6)
