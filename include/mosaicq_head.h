@@ -21,7 +21,7 @@
  * max |x| <= 448 2^e over the block, 0 where the block is all zero;
  * code = x 2^-e rounded to nearest even. A power of two rounds nothing, and
  * the matrix instruction applies it by itself. A block with an Inf or NaN has
- * the scale byte 255 (NaN) and NaN codes (127).
+ * the scale byte 255 (NaN) and NaN codes (127, also past K).
  */
 #ifndef MOSAICQ_HEAD_H
 #define MOSAICQ_HEAD_H
@@ -98,7 +98,9 @@ mq_status mq_pack8(const void* W_dev_fp16, int64_t w_stride, const mq_w8* w, voi
  * joined in a fixed order. A token's outputs depend on its own row alone, but
  * their last bits may change with M, which chooses the split. Errors:
  * MQ_ERR_INVALID_ARG (also a workspace that is too small),
- * MQ_ERR_UNSUPPORTED (sizes as mq_pack8, M >= 2^24), MQ_ERR_DEVICE.
+ * MQ_ERR_UNSUPPORTED (sizes as mq_pack8, M >= 2^24, codes_stride or
+ * scales_stride > 2^22, or 2^24 workgroups of the plan or more: about
+ * M N >= 2^39), MQ_ERR_DEVICE.
  */
 mq_status mq_linear8(const void* codes_dev, int64_t codes_stride, const void* scales_dev, int64_t scales_stride,
                      int64_t M, const mq_w8* w, void* Y_dev_fp16, int64_t y_stride, void* workspace_dev,

@@ -431,6 +431,23 @@ def test_sample_into_given_tensors_and_without_settings(hd):
     assert torch.equal(again[0], token) and torch.equal(again[1], logprob)
 
 
+def test_sample_of_more_rows_than_share_a_workspace(hd):
+    """1030 draws from one long row of logits: each as a call of fewer rows makes it, the last rows among them."""
+    import torch
+    n, V = 1030, 300001
+    l = logits(13, 1, V, "float16")
+    r = np.random.RandomState(14)
+    u, t = dev(r.rand(n).astype(np.float32)), dev(r.choice([0.0, 0.5, 1.0, 2.0], n).astype(np.float32))
+    k, p = dev(r.choice([0, 30, 1500], n).astype(np.int32)), dev(r.choice([0.5, 0.9, 1.0], n).astype(np.float32))
+    token, logprob = hd.mq_sample(l.expand(n, V), u, t, k, p)
+    for a, b in ((0, 200), (500, 501), (1000, 1030)):
+        got = hd.mq_sample(l.expand(b - a, V), u[a:b], t[a:b], k[a:b], p[a:b])
+        assert torch.equal(got[0], token[a:b]) and torch.equal(got[1], logprob[a:b])
+    at = [0, 1, 1023, 1024, 1029]
+    f = lambda x: x.cpu().numpy()[at]  # noqa: E731
+    assert list(check_rows(hd, l.expand(len(at), V), f(u), f(t), f(k), f(p))) == list(f(token))
+
+
 def test_sample_draws_in_proportion(hd):
     """Every u of a grid once: each token comes as often as its share of the grid, to one."""
     import torch
