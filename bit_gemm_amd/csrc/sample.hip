@@ -109,10 +109,12 @@ __device__ __forceinline__ double fma_c(double a, double b, double c) {
 // each by itself is a chain of 13 dependent fp64 steps. What lies beyond 2^-43 of the largest counts as that far, and gives
 // 0. (With a table of 32 and the sixth power, the constants copied: 64 x 131072 51 us, so 49.)
 constexpr int kTable = 256;
+constexpr u64 kAbove = 0x4330000000000000ull;      // the bits of 2^52
 struct Weigher {
   double top, scale;
   const double* table;     // 2^(40 + i / 256), in LDS
-  __device__ __forceinline__ u64 operator()(float l) const {
+  // with the bits of 2^52 above it
+  __device__ __forceinline__ u64 raw(float l) const {
     const double y = fmax(((double)l - top) * scale, -43.0 * kTable);
     const double n = rint(y), r = y - n;
     constexpr double c = 0.6931471805599453 / kTable;
@@ -122,8 +124,9 @@ struct Weigher {
     p = fma(p, r, 1.0);
     const int k = (int)n;
     const double w = ldexp(p * table[k & (kTable - 1)], k >> 8) + 4503599627370496.0;
-    return __builtin_bit_cast(u64, w) & 0xFFFFFFFFFFFFFull;
+    return __builtin_bit_cast(u64, w);
   }
+  __device__ __forceinline__ u64 operator()(float l) const { return raw(l) & 0xFFFFFFFFFFFFFull; }
 };
 // Fills the table; the caller's next barrier publishes it.
 __device__ __forceinline__ void fill_table(double* table) {
@@ -200,8 +203,8 @@ __device__ __forceinline__ u64 scan_group(u64 v, u64* lds, u64* all) {
   return s + sum64(lane < wave ? w : 0);
 }
 
-// What a part of a row, or the row, has: its largest logit and the first place of it, its smallest above -Inf, and
-// whether there is a logit that no row may have.
+// What a part of a row, or the row, has: its largest logit and the first place of it (of the eight tokens that hold it), its
+// smallest above -Inf, and whether there is a NaN.
 struct Range {
   float top, low;
   int first, bad;
@@ -221,16 +224,35 @@ __device__ __forceinline__ Range join_parts(const Range* p, int n) {
   if ((int)(threadIdx.x & 63) < n) a = p[threadIdx.x & 63];
   return join64(a);
 }
+// One instruction each; fmaxf of loaded values costs another to quiet each, which rows with a NaN do not need.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(d) : "v"(a), "v"(b), "v"(c));
+  return d;
+}
+__device__ __forceinline__ float min3(float a, float b, float c) {
+  float d;
+  asm("v_min3_f32 %0, %1, %2, %3" : "=v"(d) : "v"(a), "v"(b), "v"(c));
+  return d;
+}
+// By eights: `first` is where the eight tokens begin that hold the largest (token by token 17 instructions each, so 5: k_row of
+// 333 x 50257 38.7 us, so 35.4; k_top of 64 x 131072 6.7 and 5.3).
 __device__ __forceinline__ void look8(Range& a, const float* v, int at) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    a.bad |= !(v[i] < __builtin_inff());
-    if (v[i] > a.top) {
-      a.top = v[i];
-      a.first = at + i;
-    }
-    a.low = fminf(a.low, v[i] > -__builtin_inff() ? v[i] : __builtin_inff());
+  for (int i = 0; i < 8; i += 2) a.bad |= __builtin_isunordered(v[i], v[i + 1]);
+  const float top = max3(max3(v[0], v[1], v[2]), max3(v[3], v[4], v[5]), max3(v[6], v[7], v[7]));
+  if (top > a.top) {
+    a.top = top;
+    a.first = at;
   }
+  float low = min3(min3(v[0], v[1], v[2]), min3(v[3], v[4], v[5]), min3(v[6], v[7], v[7]));
+  if (low == -__builtin_inff()) {
+    float w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = v[i] > -__builtin_inff() ? v[i] : __builtin_inff();
+    low = min3(min3(w[0], w[1], w[2]), min3(w[3], w[4], w[5]), min3(w[6], w[7], w[7]));
+  }
+  a.low = min3(a.low, low, low);
 }
 
 // A row's settings, and what follows from them and its range.
@@ -254,7 +276,7 @@ __device__ __forceinline__ Row row_of(const mq_sample_args& a, int64_t r, const 
   const float t = a.temperature ? t_ : 1.0f, min_p = a.min_p ? min_p_ : 0.0f;
   x.top_k = a.top_k ? top_k_ : 0;
   x.top_p = a.top_p ? top_p_ : 1.0f;
-  x.bad = g.bad || !(g.top > -__builtin_inff()) || !(t >= 0.0f) || !(t < __builtin_inff());
+  x.bad = g.bad || !(g.top > -__builtin_inff()) || !(g.top < __builtin_inff()) || !(t >= 0.0f) || !(t < __builtin_inff());
   x.greedy = t == 0.0f;
   if (!x.greedy) x.bad |= x.top_p != x.top_p || min_p != min_p || x.u != x.u;
   x.has_k = x.top_k > 0 && x.top_k < a.vocab;
@@ -278,9 +300,15 @@ __device__ __forceinline__ void put(const mq_sample_args& a, int64_t r, int toke
   if (a.logprob) a.logprob[r] = logprob;
 }
 // Rows that have no draw: the first largest logit, or none.
-__device__ __forceinline__ bool without_draw(const mq_sample_args& a, int64_t r, const Row& x, const Range& g) {
+template <typename T>
+__device__ __forceinline__ bool without_draw(const mq_sample_args& a, int64_t r, const Row& x, const Range& g, const T* row) {
   if (!x.bad && !x.greedy) return false;
-  if (threadIdx.x == 0) put(a, r, x.bad ? -1 : g.first, x.bad ? __builtin_nanf("") : 0.0f);
+  if (threadIdx.x == 0) {
+    int token = -1;
+    if (!x.bad)
+      for (token = g.first; (float)row[token] != g.top;) ++token;      // among eight: it is there
+    put(a, r, token, x.bad ? __builtin_nanf("") : 0.0f);
+  }
   return true;
 }
 
@@ -305,13 +333,16 @@ __device__ __forceinline__ void add8(const Row& x, const float* v, u64* mass, ui
 }
 // The sum of a thread's eight weights that min_p lets in.
 __device__ __forceinline__ u64 sum8(const Row& x, const float* v) {
-  u64 m = 0;
+  u64 y[8], m = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const u64 y = x.weight(v[i]);
-    m += y >= x.least ? y : 0;
+  for (int i = 0; i < 8; ++i) y[i] = x.weight.raw(v[i]);
+  if (x.least) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = y[i] >= (kAbove | x.least) ? y[i] : kAbove;
   }
-  return m;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m += y[i];
+  return m - 8 * kAbove;
 }
 
 // Where the limits of a row fall: the steps from p0 to p1 hold the end by mass, step k that by count (kBins: none);
@@ -867,7 +898,7 @@ __global__ __launch_bounds__(kRow) void k_row(mq_sample_args a, int segs) {
   __syncthreads();
   g = join_parts(s.range, kRow / 64);
   const Row x = row_of(a, r, g, s.table);
-  if (without_draw(a, r, x, g)) return;
+  if (without_draw(a, r, x, g, row)) return;
   auto put_sum = [&](u64 m, int seg) {
     m = sum64(m);
     if (lane == 0) s.seg[seg] = m;
@@ -1000,7 +1031,7 @@ __global__ __launch_bounds__(kPick) void k_pick(mq_sample_args a, Work w) {
   const u64 sum = tid < segs ? w.seg[r * segs + tid] : 0, place = w.list[r * kList + tid];
   const Range g = join_parts(w.range + r * w.splits, w.splits);
   const Row x = row_of(a, r, g, s.table);
-  if (without_draw(a, r, x, g)) return;
+  if (without_draw(a, r, x, g, row)) return;
   if (tid < segs) s.seg[tid] = sum;
   for (int e = kPick + tid; e < segs; e += kPick) s.seg[e] = w.seg[r * segs + e];
   u64 end = ~0ull;                         // the last place that is in
