@@ -80,7 +80,10 @@ __device__ __forceinline__ uint32_t stage_pos(int lane) {
 // reads, once. The tokens' codes come from L2 through a part of LDS that is the
 // wave's own: read in the operand's order they are 16 rows an instruction, in
 // pieces of 16 bytes (16 tokens, 11008 x 4096: 12.1 us so, 10.0 through LDS).
-// The waves' sums meet in LDS and are added in their order.
+// The waves' sums meet in LDS and are added in their order. Bound by the
+// reading of the weights: 131072 x 4096, 16 tokens, 93 us (5.8 TB/s);
+// 11008 x 4096, 16 tokens, 10.0 us (4.5); 4096 x 4096, one token, 4.4 us (3.8),
+// of which 3 to begin and end.
 template <int NT, int R>
 __global__ __launch_bounds__(512) void k_stream8(Rows8 x, int M, W8 w, _Float16* y, int64_t ys) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
@@ -179,10 +182,16 @@ hipError_t go_stream(const Rows8& x, int64_t M, const W8& w, _Float16* y, int64_
 // A workgroup of 4 waves makes 64 RB weight rows x 16 TB tokens; a wave its own
 // 16 RB rows with all the tokens. The weights lie in the instruction's order,
 // so they go from L2 straight to registers; the tokens' codes go to LDS, where
-// the waves share them, by direct copies three blocks of 128 columns ahead. Steps are taken by fours, which share the words of scales;
-// what lies past K in the last four is zero in LDS and adds nothing. Nothing in
-// a step is under a condition: a load there would be waited for where the
-// branches meet.
+// the waves share them, by direct copies three blocks of 128 columns ahead
+// (one ahead, with conditions in a step and scales straight from memory, 2048
+// tokens took 505 us at 28672 x 8192, and 431 so). Steps are taken by fours, which share the words of scales; what lies past K in the last four is
+// zero in LDS and adds nothing. Nothing in a step is under a condition: a load
+// there would be waited for where the branches meet.
+// Bound by what comes from L2 and beyond it: at 28672 x 8192, 2048 tokens, 430
+// to 440 us (2.2 PFLOP/s), the matrix cores are busy half of the time, and 6.5
+// GB come through L2, a fifth of them from beyond; 4096 x 14336, 512 tokens,
+// 41 us (1.5 PFLOP/s); 10007 x 2501, 333 tokens, 17 us (1.0). Tiles of 256 x 256
+// by 8 waves, which read less, leave one workgroup a CU and were slower.
 // codes; scales of the tokens, 8 blocks of each, and of the weight rows, 4 of each; each twice
 constexpr int tiled_lds(int rb, int tokens) { return 4 * tokens * kQ8Block + 2 * (8 * tokens + 4 * 64 * rb); }
 
@@ -300,7 +309,7 @@ __global__ __launch_bounds__(256, 2) void k_tiled8(Rows8 x, int M, W8 w, _Float1
       ask_row_scales(q + 1);
       four([&](auto j) {
         const int kt = 4 * q + j;
-        weights((j + kAhead) % kSets, kt + kAhead);     // (before the copies: loads come back in order, and these are due first)
+        weights((j + kAhead) % kSets, kt + kAhead);     // before the copies: loads come back in order, and these are due first
         __builtin_amdgcn_sched_barrier(0);
         copy((j + 3) & 3, kt + 3);
         __builtin_amdgcn_sched_barrier(0);        // the loads go out first,

@@ -10,12 +10,16 @@
 // kept weights are summed by segments of the row, and the segment that the
 // draw falls into is gone through.
 //
-// One workgroup does all that for a row of up to kRowMost tokens. Longer rows go over the whole GPU: a pass of a few operations
-// over 131072 tokens takes one CU 3 us, their weights 14 us.
+// One workgroup does all that for a row of up to kRowMost tokens, or for each of kManyRows rows or more. Other rows go over
+// the whole GPU: a pass of a few operations over 131072 tokens takes one CU 3 us, their weights 14 us.
 //   k_top     the largest and smallest logit
 //   k_weigh   the histogram, or, for a row without a limit, the segments' sums
 //   k_gather  lists the tokens of the limits' steps; the sums of those above
 //   k_pick    a workgroup a row: sorts the list, finds the end, draws
+// Bound by instructions (a weight takes about 20, each of 8 a thread in turn), by chains of loads and LDS passes, and for few
+// rows by the four launches: 1 x 32000 (top_k 50, top_p) 3.5 + 4.2 + 5.9 + 6.4 us; 16 x 131072 (top_p) 4.2 + 9.8 + 8.6 + 8.0,
+// of k_weigh 5 for adding 32 histograms of a row into one; 64 x 131072 (mixed) 5.3 + 11.6 + 12.6 + 11.1. k_row: 333 x 50257
+// fp32 without a limit 35 us (1.9 TB/s of logits, which it reads twice).
 // Where the steps hold more than kList tokens (many equal logits), the limits
 // are found by a search over the digits of a key, which needs no list.
 #include "block_common.h"

@@ -212,7 +212,8 @@ def mq_sample(logits, u, temperature=None, top_k=None, top_p=None, min_p=None, t
               workspace=None, stream=None):
     """(token int32 [rows], logprob float32 [rows]): a token for each row of logits [rows, vocab] (float16 or float32)
     from uniform numbers u [rows] float32, under temperature, top_k (int32), top_p and min_p, each [rows] on the GPU or
-    None (1, and no limit). logits may be a row that is expanded (many draws from it). See mq_sample in include/mosaicq_head.h. Enqueued on `stream` (no sync)."""
+    None (1, and no limit). logits may be one row that is expanded (many draws from it). See mq_sample in
+    include/mosaicq_head.h. Enqueued on `stream` (no sync)."""
     if not isinstance(logits, torch.Tensor) or not logits.is_cuda or logits.dtype not in (_F16, torch.float32):
         raise TypeError("logits must be a float16 or float32 tensor on the GPU")
     device = logits.get_device()
