@@ -541,6 +541,45 @@ def test_the_way_out_on_other_streams_at_once(hd):
             assert all(torch.equal(a, b) for a, b in zip(g, want[i]))
 
 
+def test_two_graphs_on_one_workspace_whatever_it_holds(hd):
+    """A product split along K and long rows of logits, each captured twice on one workspace, replayed in turn over bytes of
+    any value: nothing is kept from call to call."""
+    import torch
+    r = np.random.RandomState(21)
+    p = hd.mq_pack8(dev((r.randn(64, 40000) * 0.02).astype(np.float16)))
+    rows = [hd.mq_quantize8(dev(r.randn(n, 40000).astype(np.float16))) for n in (100, 77)]
+    l = [logits(22, 5, 40000, "float16"), logits(23, 3, 70001, "float32")]
+    R = [len(x) for x in l]
+    u = [dev(r.rand(n).astype(np.float32)) for n in R]
+    k = [dev(r.choice([0, 40, 900], n).astype(np.int32)) for n in R]
+    top = [dev(np.full(n, 0.9, np.float32)) for n in R]
+    need = [max(hd.linear8_workspace(p, 100), hd.linear8_workspace(p, 77)),
+            max(hd.sample_workspace(5, 40000), hd.sample_workspace(3, 70001, True))]
+    assert min(need) > 0
+    ws = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in need]
+
+    def run(i, given=True):
+        w = ws if given else (None, None)
+        return (hd.mq_linear8(*rows[i], p, workspace=w[0]),
+                *hd.mq_sample(l[i], u[i], None, k[i], top[i], workspace=w[1]))
+
+    want = [run(i, given=False) for i in range(2)]
+    torch.cuda.synchronize()
+    graphs, out = [], []
+    for i in range(2):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[i]):
+            out.append(run(i))
+    for i in (0, 1, 1, 0, 0, 1):
+        for w in ws:
+            w.random_(0, 256)
+        for x in out[i]:
+            x.zero_()
+        graphs[i].replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out[i], want[i]))
+
+
 def test_workspaces_that_are_too_small_are_refused(hd):
     import torch
     h = Head(hd, 100, 40000, 64)                 # few outputs of long sums: split along K
