@@ -462,12 +462,12 @@ def _rows8_out(codes, scales, x, other, device: int):
     n = (W + 127) // 128
     if codes is None:        # by empty_like where it is x's shape (0.5 us faster)
         codes = (_new(other, torch.empty_like, x, dtype=_E4M3) if W == 128 * n and x.is_contiguous() else
-                 _new(other, torch.empty, (M, 128 * n), dtype=_E4M3, device=x.device))
+                 _new(other, x.new_empty, (M, 128 * n), dtype=_E4M3))
         cp, cs = codes.data_ptr(), 128 * n
     else:
         cp, cs = _matrix(codes, "codes", device, _E4M3, (M, 128 * n))
     if scales is None:
-        scales = _new(other, torch.empty, (M, n), dtype=_E8M0, device=x.device)
+        scales = _new(other, x.new_empty, (M, n), dtype=_E8M0)
         sp, ss = scales.data_ptr(), n
     else:
         sp, ss = _matrix(scales, "scales", device, _E8M0, (M, n))

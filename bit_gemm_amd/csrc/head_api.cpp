@@ -11,7 +11,7 @@ namespace {
 constexpr int64_t k31 = int64_t(1) << 31;
 constexpr int64_t kMostK = int64_t(1) << 20;
 constexpr int64_t kMostRows = int64_t(1) << 24;
-// The tiled kernel addresses a workgroup's 256 token rows by offsets under 2^30.
+// The tiled kernel addresses a workgroup's 128 token rows by offsets under 2^30.
 constexpr int64_t kMostStride = int64_t(1) << 22;
 
 mq_status from_hip(hipError_t e) {
