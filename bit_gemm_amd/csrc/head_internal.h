@@ -7,6 +7,7 @@
 #include <cstdint>
 
 #include "../../include/mosaicq_head.h"
+#include "head_plan.h"
 
 namespace mq {
 
@@ -29,18 +30,6 @@ hipError_t launch_quantize8(const _Float16* x, int64_t M, int64_t K, int64_t xs,
                             uint8_t* scales, int64_t ss, hipStream_t s);
 hipError_t launch_pack8(const _Float16* w, int64_t ws, const W8& out, hipStream_t s);
 
-// How a product is run: a rule on sizes alone (linear8.hip).
-struct Linear8Plan {
-  int nt;              // blocks of 16 tokens of the kernel that streams the weights; 0: the tiled kernel
-  int r;               // its blocks of 16 weight rows a workgroup, or of the tiled kernel a wave
-  int waves;           // its waves a workgroup
-  int tb;              // blocks of 16 tokens of the tiled kernel
-  int splits;          // of the tiled kernel along K
-  int per;             // blocks of 128 columns a split, a multiple of 4
-  int64_t groups;      // workgroups in all, of 256 threads
-  size_t bytes;        // workspace
-};
-Linear8Plan plan_linear8(int64_t M, int64_t N, int64_t K);
 hipError_t launch_linear8(const Rows8& x, int64_t M, const W8& w, _Float16* y, int64_t ys, void* ws,
                           const Linear8Plan& plan, hipStream_t s);
 

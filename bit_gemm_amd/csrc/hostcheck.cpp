@@ -1,7 +1,10 @@
-// CPU build of the packer's exact integer arithmetic (quant_exact.h), exported
-// for tests that run without a GPU. The GPU kernels compile the same header.
+// CPU build of the packer's exact integer arithmetic (quant_exact.h) and of the
+// rules by which the head's operators choose their kernels (head_plan.h),
+// exported for tests that run without a GPU. The libraries compile the same
+// headers.
 #include <cstdint>
 
+#include "head_plan.h"
 #include "quant_exact.h"
 
 #define HC_API extern "C" __attribute__((visibility("default")))
@@ -15,3 +18,16 @@ HC_API int mqh_quant7_scaled(int64_t e, uint64_t m, int Q) { return mq::quant7_s
 HC_API uint64_t mqh_err_key(uint64_t abs_e) { return mq::err_key(abs_e); }
 HC_API uint32_t mqh_fp16_div7_h(uint32_t h) { return mq::fp16_div7_h(h); }
 HC_API int mqh_quant7_f(float x, float s) { return mq::quant7_f(x, s); }
+
+// nt, r, waves, tb, splits, per of the plan; its workspace's bytes
+HC_API int64_t mqh_linear8_plan(int64_t M, int64_t N, int64_t K, int* plan) {
+  const mq::Linear8Plan p = mq::plan_linear8(M, N, K);
+  const int fields[] = {p.nt, p.r, p.waves, p.tb, p.splits, p.per};
+  for (int i = 0; i < 6; ++i) plan[i] = fields[i];
+  return (int64_t)p.bytes;
+}
+// Whether a workgroup takes a row; else a row's workgroups and the tokens of a segment.
+HC_API int mqh_sample_by_rows(int64_t rows, int64_t vocab, int* splits, int* span) {
+  mq::split(rows, vocab, splits, span);
+  return mq::by_rows(rows, vocab);
+}

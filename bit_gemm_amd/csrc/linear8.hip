@@ -400,57 +400,7 @@ hipError_t go_tiled(const Rows8& x, int64_t M, const W8& w, _Float16* y, int64_t
   return e;
 }
 
-// The tiled kernel's variants, and the time of a step of 128 columns on a CU that has nothing else, in us (MI355X, by 2 to 14
-// tiles a CU of 28672 x 8192; they are bound by what comes from L2, so a CU with two workgroups takes twice that).
-struct Variant {
-  int r, tb;
-  double step;
-};
-constexpr Variant kVariants[] = {{1, 2, 0.165}, {1, 4, 0.29}, {2, 2, 0.27}, {2, 4, 0.36}, {2, 8, 0.54}, {4, 8, 0.97}};
-
 }  // namespace
-
-// Up to 16 tokens the weights are streamed. Above, the variant with the least time by a model of what was measured over 17
-// to 2048 tokens, 1000 x 1000 to 28672 x 8192 (its choice is the fastest or within a fifth of it): 4 us to begin and end,
-// the steps of a CU's tiles one after the other, the weights from memory at 15 TB/s (what is left of it where the steps
-// cover the rest), and 5 us and the traffic of partial sums at 5 TB/s to join splits of K. Streamed: 3 us, the weights at
-// 5.2 TB/s and the tokens' codes, which each workgroup reads, at 60, by two blocks of weight rows where by one it would be
-// more workgroups than CUs (LDS holds one workgroup of 32 tokens: 6144 x 6144 10.4 us by two, 12.7 by one; 4096 x 4096 7.2
-// and 6.7), and up to 16 tokens where by two it is four a CU (8 tokens, 65536 x 2048: 24.8 and 25.5; 28672 x 8192: 44.5
-// and 42.2).
-Linear8Plan plan_linear8(int64_t M, int64_t N, int64_t K) {
-  Linear8Plan best = {};
-  const int64_t Nb = (N + 15) / 16, Kt = (K + kQ8Block - 1) / kQ8Block, Kq = (Kt + 3) / 4;
-  const double weights = (double)Nb * Kt * kTile;
-  double least = 1e30;
-  if (M <= 32) {
-    best.nt = M <= 16 ? 1 : 2;
-    best.r = Nb > (M <= 16 ? 2047 : 256) ? 2 : 1;
-    best.waves = (int)(Kq < 8 ? Kq : 8);
-    best.groups = 2 * ((Nb + best.r - 1) / best.r);     // of 512 threads
-    least = 3.0 + weights / 5.2e6 + (double)Nb / best.r * 16.0 * best.nt * K / 60e6;
-    if (M <= 16) return best;
-  }
-  for (const Variant& v : kVariants) {
-    const int64_t T = ((Nb + 4 * v.r - 1) / (4 * v.r)) * ((M + 16 * v.tb - 1) / (16 * v.tb));
-    for (int64_t S : {1, 2, 3, 4, 8}) {
-      if (S > 1 && (S > Kq || T * S > 1024)) break;
-      const int64_t per = (Kq + S - 1) / S, splits = (Kq + per - 1) / per, a_cu = (T * splits + 255) / 256;
-      double t = 4.0 + 4.0 * per * a_cu * v.step + weights / 15e6;
-      if (splits > 1) t += 5.0 + 8.0 * splits * M * N / 5e6;
-      if (t >= least) continue;
-      least = t;
-      best = {};
-      best.r = v.r;
-      best.tb = v.tb;
-      best.splits = (int)splits;
-      best.per = (int)(4 * per);
-      best.groups = T * splits;
-      if (splits > 1) best.bytes = (size_t)splits * M * N * sizeof(float);
-    }
-  }
-  return best;
-}
 
 hipError_t launch_linear8(const Rows8& x, int64_t M, const W8& w, _Float16* y, int64_t ys, void* ws,
                           const Linear8Plan& p, hipStream_t s) {

@@ -35,13 +35,9 @@ constexpr float kReach = 28.5f;            // exp(-28.5) < 2^-41: no weight beyo
 constexpr int kBins = 2048;
 constexpr int kList = 2048;                // tokens that a workgroup sorts
 constexpr int kFewest = 1024;              // a top_k up to this is listed whole, and needs no masses
-constexpr int kGroup = 512, kGroupWaves = kGroup / 64;      // k_top, k_weigh, k_gather
+constexpr int kGroup = 64 * kGroupWaves;   // k_top, k_weigh, k_gather
 constexpr int kPick = 256;                 // k_pick: what runs once costs each wave of a SIMD its issue slots
 constexpr int kRow = 512;                  // k_row
-constexpr int kMostSegs = 512;             // segments of a row
-constexpr int64_t kRowMost = 16384;        // tokens of a row that one workgroup takes,
-constexpr int64_t kRowMostEach = 320;      // of several rows this many times the rows,
-constexpr int64_t kManyRows = 192, kManyMost = 512 * kMostSegs;      // and of each of many rows
 constexpr int64_t kRowsAtOnce = 1024;      // rows that share the workspace
 
 // Eight logits as they lie, asked for and not waited for; -Inf where the row has ended.
@@ -1057,29 +1053,6 @@ __global__ __launch_bounds__(kPick) void k_pick(mq_sample_args a, Work w) {
 }
 
 // ------------------------------------------------------------------- the host
-// Segments of a row, of 512 tokens at least: so many that about kGroups workgroups share the rows, and a wave's lanes can
-// hold what each workgroup of a row found. (With 256 workgroups 64 x 131072 takes 49 us, so 43.5; 16 x 131072 28.7 and 30.4:
-// there the joining of 32 histograms a row takes half of k_weigh.)
-constexpr int64_t kGroups = 512;
-
-void split(int64_t rows, int64_t vocab, int* splits, int* span) {
-  int64_t s = 512;
-  auto groups = [&] { return (vocab + kGroupWaves * s - 1) / (kGroupWaves * s); };
-  while (groups() > kMostSegs / kGroupWaves || (groups() > 1 && rows * groups() > kGroups)) s *= 2;
-  *span = (int)s;
-  *splits = (int)groups();
-}
-
-// Whether a workgroup takes a row. It takes the same time however many others there are, up to one a CU; over the whole GPU
-// rows share it. By rows and over the GPU, in us, top-k 50 with top-p 0.9 and top-p alone: 1 row of 16384 16.1 and 18.2,
-// 18.7 and 18.6; of 20000 17.6 and 18.7, 21.7 and 18.4; 64 of 20000 18.8 and 24.1, 22.7 and 25.9; of 32000 23.1 and 26.1,
-// 30.3 and 28.8; 128 of 32000 23.2 and 27.3, 30.5 and 32.8; of 50257 31.3 and 30.7, 42.9 and 38.6; 192 of 50257 31.1 and
-// 40.1, 43.0 and 56.0.
-bool by_rows(int64_t rows, int64_t vocab) {
-  if (rows >= kManyRows) return vocab <= kManyMost;
-  return vocab <= kRowMost || vocab <= kRowMostEach * rows;
-}
-
 size_t up16(size_t n) { return (n + 15) & ~size_t(15); }
 
 // The workspace of so many rows at once; base may be null, for its size alone.
