@@ -1,4 +1,4 @@
-"""Sizes at which the head's product takes each of its kernels. What they take is checked without a GPU
+"""Sizes at which the head's operators take each of their kernels. What they take is checked without a GPU
 (test_head_plans_cpu.py); the results are checked on one (test_gpu_head_kernels.py)."""
 import ctypes
 import os
@@ -37,12 +37,20 @@ LINEAR = [
     ((2063, 450, 14189), ("tiled", 4, 8, 7)),
 ]
 
+# mq_sample: (rows, vocab), and whether a workgroup takes a row; both sides of each border
+SAMPLE = [
+    ((1, 16384), True), ((1, 16385), False), ((64, 20000), True), ((64, 20480), True), ((64, 20481), False),
+    ((100, 32000), True), ((191, 61120), True), ((191, 61121), False), ((200, 50257), True), ((192, 262144), True),
+    ((192, 262145), False),
+]
+
 
 def _lib():
     assert os.path.exists(HC), "libmq_hostcheck.so is not built"
     h = ctypes.CDLL(HC)
     i64, ints = ctypes.c_int64, ctypes.POINTER(ctypes.c_int)
     h.mqh_linear8_plan.argtypes, h.mqh_linear8_plan.restype = [i64, i64, i64, ints], i64
+    h.mqh_sample_by_rows.argtypes, h.mqh_sample_by_rows.restype = [i64, i64, ints, ints], ctypes.c_int
     return h
 
 
@@ -52,3 +60,10 @@ def linear_kernel(M, N, K):
     n = _lib().mqh_linear8_plan(M, N, K, plan)
     nt, r, _, tb, splits, _ = plan
     return (("stream", nt, r) if nt else ("tiled", r, tb, splits)), n
+
+
+def sample_by_rows(rows, vocab):
+    """Whether a workgroup takes a row; a row's workgroups and the tokens of a segment where not."""
+    splits, span = ctypes.c_int(), ctypes.c_int()
+    by_rows = bool(_lib().mqh_sample_by_rows(rows, vocab, ctypes.byref(splits), ctypes.byref(span)))
+    return by_rows, splits.value, span.value

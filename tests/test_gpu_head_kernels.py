@@ -1,4 +1,4 @@
-"""Every kernel of the head's product at sizes that use its stages, buffers and segments more than once (head_cases.py says
+"""Every kernel of the head's operators at sizes that use its stages, buffers and segments more than once (head_cases.py says
 which size takes which; test_head_plans_cpu.py that it does).
 
 Exact: the products of small whole numbers. Elements are q 2^j with |q| <= 2, j of their block of 128 in 0 .. 2 (tokens) or
@@ -6,7 +6,8 @@ Exact: the products of small whole numbers. Elements are q 2^j with |q| <= 2, j 
 and with K < 2^15 every sum is a whole number under 2^20, which fp32 holds. So Y is the whole number, rounded once to fp16,
 in whatever order it is summed.
 
-Tolerance of the other products as in test_gpu_head.py.
+Tolerance of the other products as in test_gpu_head.py. Tokens are exact; log-probabilities of the same row by two kernels are
+the same bits (whole weights and sums, one logarithm of their quotient).
 """
 import math
 
@@ -16,7 +17,7 @@ import pytest
 from oracle import head as oh
 from tests import head_cases as hc
 from tests.test_gpu_block import SUB, U, close, dev
-from tests.test_gpu_head import halves, hd  # noqa: F401  (the fixture)
+from tests.test_gpu_head import SETTINGS, halves, hd  # noqa: F401  (the fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -115,9 +116,105 @@ def test_products_of_rows_of_any_size(hd, case, kernel):  # noqa: F811
     close(y[dev(ms)][:, dev(ns)].cpu().numpy(), want, tol, f"{M} x {N} x {K}")
 
 
-# --------------------------------------------------------------------- refusals
-def test_a_workspace_that_is_too_small_is_refused(hd):  # noqa: F811
+# -------------------------------------------------------------------- sampling
+def rows_of_settings(R, r):
+    pick = r.randint(0, len(SETTINGS), R)
+    t, k, p, m = (np.array([SETTINGS[i][j] for i in pick], dt) for j, dt in
+                  ((0, np.float32), (1, np.int32), (2, np.float32), (3, np.float32)))
+    u = r.rand(R).astype(np.float32)
+    u[r.rand(R) < 0.1], u[r.rand(R) < 0.1] = 0.0, 1.0 - 2.0 ** -24
+    return u, t, k, p, m
+
+
+def check(hd, l, settings, some_rows, alone):  # noqa: F811
+    """All rows by one call, some against the oracle, all (in turn) against calls of `alone` rows."""
     import torch
+    R, V = l.shape
+    on = [dev(a) for a in settings]
+    token, logprob = hd.mq_sample(l, *on)
+    for i in some_rows:
+        u, t, k, p, m = (a[i] for a in settings)
+        want, lp, kept = oh.sample(l[i].float().cpu().numpy(), u, t, int(k), p, m)
+        assert token[i].item() == want, f"row {i}: token {token[i].item()}, want {want} of {len(kept)} kept"
+        assert abs(logprob[i].item() - lp) <= 2.0 ** -23 * abs(lp) + 2.0 ** -40 * V
+    for a in range(0, R, alone):
+        got = hd.mq_sample(l[a:a + alone], *(x[a:a + alone] for x in on))
+        assert torch.equal(got[0], token[a:a + alone]) and torch.equal(got[1], logprob[a:a + alone]), f"rows {a} .."
+
+
+def spread_logits(R, V, dtype, seed):
+    """Rows of several kinds: normal of any sharpness, half or almost all of it masked, few values, one narrow step."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    l = torch.randn((R, V), generator=g, device="cuda")
+    l *= torch.exp2(torch.randint(-1, 3, (R, 1), generator=g, device="cuda").float())
+    for i in range(1, R, 6):
+        l[i, torch.rand(V, generator=g, device="cuda") < 0.5] = -math.inf
+    for i in range(2, R, 6):
+        l[i, torch.rand(V, generator=g, device="cuda") < 0.999] = -math.inf
+        l[i, V - 1] = 0.25
+    for i in range(3, R, 6):                   # many equal logits around every limit
+        l[i] = torch.randint(-2, 3, (V,), generator=g, device="cuda").float()
+    for i in range(4, R, 6):                   # many that differ in their last bits
+        l[i] = 1.0 + torch.randint(0, 3000, (V,), generator=g, device="cuda").float() * 2.0 ** -22
+    return l.half() if dtype == "float16" else l
+
+
+@pytest.mark.parametrize("dtype", ["float16", "float32"])
+@pytest.mark.parametrize("case,by_rows", hc.SAMPLE, ids=["%dx%d" % c for c, _ in hc.SAMPLE])
+def test_sample_on_both_sides_of_the_rules(hd, case, by_rows, dtype):  # noqa: F811
+    """Each row the same by a workgroup and over the whole GPU, and as the oracle draws it."""
+    R, V = case
+    r = np.random.RandomState(R + V)
+    alone = next(n for n in (40, 9, 5, 3, 1) if n < R or R == 1)
+    if R > 1:
+        assert hc.sample_by_rows(alone, V)[0] is False
+    few = [0, R - 1, *r.randint(0, R, 5)] if V < 100000 else [3, R - 1]
+    check(hd, spread_logits(R, V, dtype, V), rows_of_settings(R, r), sorted(set(few)), alone)
+
+
+@pytest.mark.parametrize("dtype", ["float16", "float32"])
+@pytest.mark.parametrize("R,V", [(64, 20000), (200, 50257), (4, 50257), (2, 262145), (1, 1 << 20)])
+def test_sample_where_more_tokens_tie_than_a_list_holds(hd, R, V, dtype):  # noqa: F811
+    """Limits by count and by mass that end inside a run of 4000 equal logits and more: found by the search over digits."""
+    import torch
+    r = np.random.RandomState(V)
+    g = torch.Generator(device="cuda").manual_seed(V)
+    run = 4000
+    l = torch.randn((R, V), generator=g, device="cuda") - 6.0
+    for i in range(R):
+        at = torch.randperm(V, generator=g, device="cuda")
+        l[i, at[:run]] = 1.5
+        l[i, at[run:run + 60]] = 2.0 + torch.rand(60, generator=g, device="cuda")
+    l = l.half() if dtype == "float16" else l
+    k = np.where(np.arange(R) % 3 < 2, r.randint(100, run, R), 0).astype(np.int32)     # inside the run; none
+    p = np.where(np.arange(R) % 3 > 0, r.uniform(0.3, 0.8, R), 1.0).astype(np.float32)
+    if R == 1:
+        k[:], p[:] = 2500, 0.5
+    s = (r.rand(R).astype(np.float32), np.ones(R, np.float32), k, p, np.where(np.arange(R) % 2, 0.01, 0).astype(np.float32))
+    few = sorted({0, 1 % R, 2 % R, R - 1}) if V <= 262145 else [0]
+    check(hd, l, s, few, 40 if R > 40 else 1)
+
+
+@pytest.mark.parametrize("R,V", [(192, 100003), (192, 262144), (5, 262145)])
+def test_sample_draws_from_every_segment(hd, R, V):  # noqa: F811
+    """Equal logits: the token is floor(u V), wherever in the row it lies, for a row by a workgroup and over the GPU."""
+    import torch
+    u = (np.arange(R) / R + 1e-4).astype(np.float32)
+    token, logprob = hd.mq_sample(torch.zeros((1, V), dtype=torch.float16, device="cuda").expand(R, V), dev(u))
+    want = [int(float(x) * 2 ** 31) * V >> 31 for x in u]       # u counts in steps of 2^-31
+    assert token.tolist() == want
+    assert torch.allclose(logprob, torch.full_like(logprob, -math.log(V)), rtol=2.0 ** -23, atol=2.0 ** -23)
+
+
+# --------------------------------------------------------------------- refusals
+def test_workspaces_that_are_too_small_are_refused_where_one_is_needed(hd):  # noqa: F811
+    import torch
+    l = torch.zeros((2, 300000), dtype=torch.float16, device="cuda")
+    need = hd.sample_workspace(2, 300000)
+    assert need > 0
+    with pytest.raises(hd.MQError):
+        hd.mq_sample(l, torch.rand(2, device="cuda"), workspace=torch.empty(need - 16, dtype=torch.uint8, device="cuda"))
     M, N, K = 359, 962, 17050
     p = hd.mq_pack8(dev(halves(1, (N, K), 1)))
     need = hd.linear8_workspace(p, M)

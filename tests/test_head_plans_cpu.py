@@ -33,3 +33,13 @@ def test_every_linear_kernel_is_among_them():
         assert k[:3] in {x[:3] for x in kernels}, (M, N, K, k)
     for (_, N, K), k in hc.LINEAR:
         assert N % 4 and -(-K // 128) >= 11
+
+
+@pytest.mark.parametrize("case,by_rows", hc.SAMPLE)
+def test_sample_kernels(hd, case, by_rows):  # noqa: F811
+    got, splits, span = hc.sample_by_rows(*case)
+    assert got == by_rows
+    a, n = hd._SampleArgs(rows=case[0], vocab=case[1]), ctypes.c_size_t()
+    assert hd.lib.mq_sample_workspace(ctypes.byref(a), ctypes.byref(n)) == 0
+    assert (n.value == 0) == by_rows
+    assert splits <= 64 and 8 * splits * span >= case[1]
