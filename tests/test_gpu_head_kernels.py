@@ -6,8 +6,8 @@ Exact: the products of small whole numbers. Elements are q 2^j with |q| <= 2, j 
 and with K < 2^15 every sum is a whole number under 2^20, which fp32 holds. So Y is the whole number, rounded once to fp16,
 in whatever order it is summed.
 
-Tolerance of the other products as in test_gpu_head.py. Tokens are exact; log-probabilities of the same row by two kernels are
-the same bits (whole weights and sums, one logarithm of their quotient).
+Tolerance of the other products: the bound that mosaicq_head.h states, which is that of test_gpu_head.py. Tokens are exact;
+log-probabilities of the same row by two kernels are the same bits (whole weights and sums, one logarithm of their quotient).
 """
 import math
 
@@ -85,6 +85,11 @@ def test_products_in_a_graph(hd, case):  # noqa: F811
         assert torch.equal(got, hd.mq_linear8(codes, scales, p))
 
 
+def bound(want, top, mag, K8):
+    """What mosaicq_head.h lets a product be off by."""
+    return U * np.abs(want) + SUB + 7 * 2.0 ** -13 * top + 2.0 ** -19 * (K8 / 128 + 1) * mag
+
+
 def some(n, count, r):
     """The first, the last and some others of n."""
     return np.unique(np.r_[0, n - 1, r.randint(0, n, count)])
@@ -112,8 +117,62 @@ def test_products_of_rows_of_any_size(hd, case, kernel):  # noqa: F811
     ms, ns = (i[i != skip] for i, skip in ((some(M, 7, r), M // 2), (some(N, 14, r), N // 3)))
     xv, wv = (oh.held(*oh.rows8(t[dev(i)].cpu().numpy())) for t, i in ((x, ms), (W, ns)))
     want, top, mag = oh.linear8(xv, wv)
-    tol = U * np.abs(want) + SUB + 7 * 2.0 ** -13 * top + (16 * xv.shape[1] / 128 + 16) * 2.0 ** -23 * mag
-    close(y[dev(ms)][:, dev(ns)].cpu().numpy(), want, tol, f"{M} x {N} x {K}")
+    close(y[dev(ms)][:, dev(ns)].cpu().numpy(), want, bound(want, top, mag, xv.shape[1]), f"{M} x {N} x {K}")
+
+
+def product_of(hd, x, W, what):  # noqa: F811
+    y = hd.mq_linear8(*hd.mq_quantize8(dev(x)), hd.mq_pack8(dev(W))).cpu().numpy()
+    xv, wv = oh.held(*oh.rows8(x)), oh.held(*oh.rows8(W))
+    want, top, mag = oh.linear8(xv, wv)
+    close(y, want, bound(want, top, mag, xv.shape[1]), what)
+    return y, want
+
+
+@pytest.mark.parametrize("M", [5, 30, 70, 200])
+@pytest.mark.parametrize("kind", ["one size", "many sizes", "just under the cut"])
+def test_products_of_one_sign(hd, kind, M):  # noqa: F811
+    """Cuts that all go the same way. In the last kind seven products of each group of 8 are cut whole."""
+    N, K = 20, 5001
+    r = np.random.RandomState(M)
+    if kind == "just under the cut":
+        x, W = np.full((M, K), 2.0), np.full((N, K), 3.75)
+        x[:, ::8] = W[:, ::8] = 256.0                     # 2^16, and 7.5 where all under 2^3 is cut
+        W *= 2.0 ** -18
+    else:
+        x, W = (2.0 ** r.uniform(0, 1, s) if kind == "one size" else 2.0 ** r.uniform(-6, 6, s) for s in ((M, K), (N, K)))
+        W *= 2.0 ** -8
+    y, want = product_of(hd, x.astype(np.float16), W.astype(np.float16), kind)
+    assert (np.abs(y - want) <= (7 * 2.0 ** -13 + U + 2.0 ** -19 * 41) * want).all()
+
+
+@pytest.mark.parametrize("M", [5, 30, 70, 200])
+@pytest.mark.parametrize("apart", [1, 4, 1280])
+def test_products_that_cancel(hd, M, apart):  # noqa: F811
+    """Every product but the last block's comes again with the other sign, in its own group of 8 or in another block."""
+    N, K = 20, 2560
+    r = np.random.RandomState(M + apart)
+    x, W = np.zeros((M, K + 128)), np.zeros((N, K + 128))
+    first = np.arange(K).reshape(-1, 2, apart)[:, 0].ravel()
+    for t, sign in ((x, 1), (W, -1)):
+        t[:, first] = r.randn(len(t), K // 2)
+        t[:, first + apart] = sign * t[:, first]
+        t[:, K:] = r.randn(len(t), 128) * 2.0 ** -4
+    product_of(hd, x.astype(np.float16), W.astype(np.float16), f"{apart} apart")
+
+
+@pytest.mark.parametrize("M", [1, 40])
+def test_the_longest_sums(hd, M):  # noqa: F811
+    """K of 2^20, one sign; the first and the last token."""
+    import torch
+    N, K = 3, 1 << 20
+    g = torch.Generator(device="cuda").manual_seed(M)
+    x, W = ((1 + torch.rand((n, K), generator=g, device="cuda")).half() for n in (M, N))
+    W *= 2.0 ** -14
+    y = hd.mq_linear8(*hd.mq_quantize8(x), hd.mq_pack8(W)).cpu().numpy()
+    ms = sorted({0, M - 1})
+    xv, wv = (oh.held(*oh.rows8(t.cpu().numpy())) for t in (x[ms], W))
+    want, top, mag = oh.linear8(xv, wv)
+    close(y[ms], want, bound(want, top, mag, K), f"{M} tokens")
 
 
 # -------------------------------------------------------------------- sampling
