@@ -478,7 +478,8 @@ def mq_norm_residual_q8(y, r, w_pre, w_post=None, gate=None, alpha: float = 1.0,
                         weight_offset: float = 0.0, r_out=None, codes_out=None, scales_out=None, stream=None):
     """(r', codes, scales): mq_norm_residual with h = norm(r') (w_pre + offset) as 8-bit rows, for head.mq_linear8.
     codes float8_e4m3fn [tokens, 128 n] and scales float8_e8m0fnu [tokens, n], n = ceil(width / 128): a power of two
-    for each block of 128 elements, zeros past width. Enqueued on `stream` (no sync)."""
+    for each block of 128 elements, zeros past width (all codes of a block with an Inf or NaN are NaN, its scale too).
+    Enqueued on `stream` (no sync)."""
     if not isinstance(r, torch.Tensor) or not r.is_cuda or r.dtype not in (_F16, torch.float32):
         raise TypeError("r must be a float16 or float32 tensor on the GPU")
     device = r.get_device()

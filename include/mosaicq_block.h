@@ -245,7 +245,8 @@ mq_status mq_norm_residual(const mq_norm_args* args, void* hip_stream);
  *
  *   args         as above with w_pre; h_out is the codes, [tokens, K8] bytes,
  *                K8 = 128 ceil(width / 128), 16-byte aligned, rows h_stride bytes
- *                apart (>= K8, a multiple of 16); bytes past width, up to K8, are 0
+ *                apart (>= K8, a multiple of 16); bytes past width, up to K8, are 0,
+ *                in a block with an Inf or NaN 127 (NaN) like its other codes
  *   scales_dev   [tokens, K8 / 128] bytes, rows scales_stride bytes apart
  *
  * Errors as mq_norm_residual, and MQ_ERR_INVALID_ARG without w_pre.

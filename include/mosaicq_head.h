@@ -84,7 +84,8 @@ mq_status mq_pack8(const void* W_dev_fp16, int64_t w_stride, const mq_w8* w, voi
  *   codes_dev, scales_dev   [M, K8] and [M, K8 / 128] as mq_quantize8 writes
  *                them, rows codes_stride and scales_stride bytes apart; codes
  *                16-byte aligned with a stride that is a multiple of 16; codes
- *                past K are multiplied by zero weights and have to be no NaN
+ *                past K are multiplied by zero weights: a NaN among them (as in a
+ *                block that is NaN anyway) makes the token's outputs NaN
  *   M            tokens, >= 0 (0 enqueues nothing)
  *   w            from mq_pack8
  *   Y_dev_fp16   [M, N], rows y_stride elements apart (>= N), 2-byte aligned

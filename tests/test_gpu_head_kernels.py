@@ -175,6 +175,25 @@ def test_the_longest_sums(hd, M):  # noqa: F811
     close(y[ms], want, bound(want, top, mag, K), f"{M} tokens")
 
 
+@pytest.mark.parametrize("K", [1, 200, 1281])
+def test_blocks_that_are_not_finite_are_nan_up_to_their_end(hd, K):  # noqa: F811
+    """By the quantizer and by the norm: all codes of such a block are 127, also past the row's end; other blocks are as ever,
+    and 0 past the row's end."""
+    import torch
+    from bit_gemm_amd import block as bk
+    x = torch.ones((4, K), device="cuda")
+    x[1, K - 1], x[2, 0] = math.inf, math.nan
+    n = -(-K // 128)
+    for codes, scales in (hd.mq_quantize8(x.half()),
+                          bk.mq_norm_residual_q8(None, x, torch.ones(K, dtype=torch.float16, device="cuda"))[1:]):
+        c, s = (t.view(torch.uint8).cpu().numpy() for t in (codes, scales))
+        assert c.shape == (4, 128 * n) and (c[0, K:] == 0).all() and (c[3, K:] == 0).all() and (s[[0, 3]] == 119).all()
+        assert (c[1, 128 * (n - 1):] == 127).all() and s[1, n - 1] == 255
+        assert (c[2, :128] == 127).all() and s[2, 0] == 255
+        if n > 1:
+            assert (c[2, K:] == 0).all() or s[2, n - 1] == 255       # the norm spreads a NaN over its row
+
+
 # -------------------------------------------------------------------- sampling
 def rows_of_settings(R, r):
     pick = r.randint(0, len(SETTINGS), R)
