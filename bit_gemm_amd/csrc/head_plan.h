@@ -22,7 +22,7 @@ struct Linear8Plan {
 };
 
 // The tiled kernel's variants, and the time of a step of 128 columns on a CU that has nothing else, in us (MI355X, by 2 to 14
-// tiles a CU of 28672 x 8192; they are bound by what comes from L2, so a CU with two workgroups takes twice that).
+// tiles a CU of 28672 x 8192, two workgroups at a time, which take twice that each).
 struct Variant {
   int r, tb;
   double step;
@@ -36,7 +36,7 @@ constexpr Variant kVariants[] = {{1, 2, 0.165}, {1, 4, 0.29}, {2, 2, 0.27}, {2, 
 // 5.2 TB/s and the tokens' codes, which each workgroup reads, at 60, by two blocks of weight rows where by one it would be
 // more workgroups than CUs (LDS holds one workgroup of 32 tokens: 6144 x 6144 10.4 us by two, 12.7 by one; 4096 x 4096 7.2
 // and 6.7), and up to 16 tokens where by two it is four a CU (8 tokens, 65536 x 2048: 24.8 and 25.5; 28672 x 8192: 44.5
-// and 42.2).
+// and 42.2). Up to 16 tokens nothing is compared: narrow layers with a long K stay on few CUs (128 x 16384 6.6 us for 2 MB).
 inline Linear8Plan plan_linear8(int64_t M, int64_t N, int64_t K) {
   Linear8Plan best = {};
   const int64_t Nb = (N + 15) / 16, Kt = (K + 127) / 128, Kq = (Kt + 3) / 4;

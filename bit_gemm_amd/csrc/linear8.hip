@@ -87,9 +87,11 @@ __device__ __forceinline__ uint32_t stage_pos(int lane) {
 // wave's own: read in the operand's order they are 16 rows an instruction, in
 // pieces of 16 bytes (16 tokens, 11008 x 4096: 12.1 us so, 10.0 through LDS).
 // The waves' sums meet in LDS and are added in their order. Bound by the
-// reading of the weights: 131072 x 4096, 16 tokens, 93 us (5.8 TB/s);
-// 11008 x 4096, 16 tokens, 10.0 us (4.5); 4096 x 4096, one token, 4.4 us (3.8),
-// of which 3 to begin and end.
+// reading of the weights: 131072 x 4096, 16 tokens, 94 us (5.8 TB/s);
+// 11008 x 4096, 16 tokens, 10.2 us (4.5); 4096 x 4096, one token, 4.3 us (3.9),
+// of which 3 to begin and end. (Averages of traced calls.) Where a layer has few
+// rows and a long K, the few workgroups are what binds: 128 x 16384, 16 tokens,
+// 6.6 us for 2 MB on 8 CUs; 128 x 65536 20 us.
 template <int NT, int R>
 __global__ __launch_bounds__(512) void k_stream8(Rows8 x, int M, W8 w, _Float16* y, int64_t ys) {
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
@@ -190,14 +192,21 @@ hipError_t go_stream(const Rows8& x, int64_t M, const W8& w, _Float16* y, int64_
 // so they go from L2 straight to registers; the tokens' codes go to LDS, where
 // the waves share them, by direct copies three blocks of 128 columns ahead
 // (one ahead, with conditions in a step and scales straight from memory, 2048
-// tokens took 505 us at 28672 x 8192, and 431 so). Steps are taken by fours, which share the words of scales; what lies past K in the last four is
+// tokens took 505 us at 28672 x 8192, and about 440 so). Steps are taken by
+// fours, which share the words of scales; what lies past K in the last four is
 // zero in LDS and adds nothing. Nothing in a step is under a condition: a load
 // there would be waited for where the branches meet.
-// Bound by what comes from L2 and beyond it: at 28672 x 8192, 2048 tokens, 430
-// to 440 us (2.2 PFLOP/s), the matrix cores are busy half of the time, and 6.5
-// GB come through L2, a fifth of them from beyond; 4096 x 14336, 512 tokens,
-// 41 us (1.5 PFLOP/s); 10007 x 2501, 333 tokens, 17 us (1.0). Tiles of 256 x 256
-// by 8 waves, which read less, leave one workgroup a CU and were slower.
+// What it spends its time on, by the same kernel with parts left out (us; whole,
+// without loads in the loop, without products, without either, and with the same
+// four tiles asked for again and again, so that little comes from beyond L2):
+//   28672 x 8192, 2048 tokens  440 (2.2 PFLOP/s)  276  381  168  389
+//   4096 x 14336, 512 tokens   42 (1.4; 55 where the weights come from HBM)  28  49  32  37
+//   10007 x 2501, 333 tokens   18 (0.9)  13.5  18  14  16.5
+// Much work: the loads through L2, which the products cover in part; what lies
+// beyond L2 is an eighth. One round of tiles: mostly a step by itself, its LDS
+// reads, products and barrier with one workgroup of four waves a CU. (Without
+// products, what takes their place to use the operands costs some time.) Tiles of
+// 256 x 256 by 8 waves leave one workgroup a CU and were slower.
 // codes; scales of the tokens, 8 blocks of each, and of the weight rows, 4 of each; each twice
 constexpr int tiled_lds(int rb, int tokens) { return 4 * tokens * kQ8Block + 2 * (8 * tokens + 4 * 64 * rb); }
 

@@ -16,12 +16,16 @@
 //   k_weigh   the histogram, or, for a row without a limit, the segments' sums
 //   k_gather  lists the tokens of the limits' steps; the sums of those above
 //   k_pick    a workgroup a row: sorts the list, finds the end, draws
-// Bound by instructions (a weight takes about 20, each of 8 a thread in turn), by chains of loads and LDS passes, and for few
-// rows by the four launches: 1 x 32000 (top_k 50, top_p) 3.5 + 4.2 + 5.9 + 6.4 us; 16 x 131072 (top_p) 4.2 + 9.8 + 8.6 + 8.0,
-// of k_weigh 5 for adding 32 histograms of a row into one; 64 x 131072 (mixed) 5.3 + 11.6 + 12.6 + 11.1. k_row: 333 x 50257
-// fp32 without a limit 35 us (1.9 TB/s of logits, which it reads twice).
-// Where the steps hold more than kList tokens (many equal logits), the limits
-// are found by a search over the digits of a key, which needs no list.
+// Few rows are bound by the launches, each a chain of loads, LDS passes and barriers: 1 x 32000 (top_k 50, top_p) 3.4 + 4.2 +
+// 6.0 + 6.5 us; 16 x 131072 (top_p) 4.1 + 10.3 + 8.7 + 8.1, of k_weigh 5 for adding 32 histograms of a row into one. More rows:
+// 64 x 131072 (mixed) 5.3 + 11.7 + 12.5 + 11.1, of which the vector instructions (a weight takes about 20) would be 12 if they
+// followed each other; the rest, those chains, was not taken apart. k_row: 333 x 50257 fp32 without a limit 35 us (1.9 TB/s of
+// logits, which it reads twice), its instructions 15 spread evenly, but 77 of the 256 CUs hold two rows; 1 row of 16384 9 us
+// without a limit, 16 to 20 with: one CU's passes.
+// Where the steps hold more than kList tokens, the limits are found by a search over the digits of a key, which needs no list:
+// rows with more equal logits than that at a limit, and ordinary rows from some 10^6 tokens on. That is slow: a row by one
+// workgroup, and equal logits add to one counter in turn. 50257 equal logits 0.35 ms (0.62 with both limits; 200 rows 0.39 and
+// 0.66), 2^20 6 and 11 ms, 2^22 25 and 46 ms; 2^22 normal logits with top_p 11 ms.
 #include "block_common.h"
 #include "head_internal.h"
 
